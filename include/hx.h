@@ -329,6 +329,108 @@ int hx_session_drain(hx_session* s);
 int hx_session_batch_info(const hx_session* s, uint64_t batch, hx_batch_info* out);
 void hx_session_destroy(hx_session* s);
 
+/* ---- 8-bit rows --------------------------------------------------------------------------
+ * Where the coder's symbols come from and go to in a training step: a matrix of activations (or
+ * weights) kept as one byte per value and one 32-bit scale per row, and the operators of a
+ * backward pass that read their saved inputs in this form. The bytes of a matrix are contiguous
+ * (rows * cols), so they are what hx_encode takes and hx_decode gives back.
+ *
+ * Value = byte's value * the row's scale.
+ *   HX_ROWS_E4M3  s = the smallest power of two with absmax / s <= 448, within 2^-126 .. 2^119 (a
+ *                 byte times its scale is exact). Bytes: x / s to e4m3, ties to even, saturating.
+ *   HX_ROWS_INT8  s = absmax / 127 within 2^-126 .. 2^121 (32-bit division); bytes: x / s (32-bit
+ *                 division) to the nearest integer, ties to even, within +-127.
+ * A row of zeros has scale 1. A row with a NaN or an infinity has scale NaN and bytes 0, so that
+ * every value read from it is NaN.
+ *
+ * Rules of this section. Element types are HX_F32, HX_F16, HX_BF16; bytes have no alignment rule,
+ * everything else its element's alignment (rows that start on 16 bytes, and bytes on 8, are read in
+ * vectors). `ld` and the other strides are in elements; a stride of one row or token is not looked
+ * at. Outputs do not overlap inputs, unless a call says so. rows = 0 (tokens = 0) is allowed and
+ * touches only what the call says. cols < 2^30, rows < 2^31, at most 2^40 values. Arithmetic is in
+ * 32 bits, each output rounded once. Results do not depend on the launch (no atomics on values). */
+enum { HX_F32 = 0, HX_F16 = 1, HX_BF16 = 2 };
+enum { HX_ROWS_E4M3 = 0, HX_ROWS_INT8 = 1 };
+
+/* Rows of d_x (rows x cols, row stride ld) to d_bytes (rows * cols) and d_scale (f32[rows]). */
+int hx_quantize_rows(uint32_t format, uint32_t dtype, const void* d_x, uint64_t rows, uint64_t cols,
+                     uint64_t ld, uint8_t* d_bytes, float* d_scale, void* stream);
+
+/* The reverse: d_out (rows x cols, row stride ld). An f16 output stays within +-65504 for a finite
+ * scale (a value just below can round above it in its byte). */
+int hx_dequantize_rows(uint32_t format, uint32_t dtype, const uint8_t* d_bytes,
+                       const float* d_scale, uint64_t rows, uint64_t cols, void* d_out, uint64_t ld,
+                       void* stream);
+
+/* The gated activation of a feed-forward layer, saved as 8-bit rows. d_x: rows x 2 cols (row stride
+ * ld >= 2 cols), a row's gate g in its first cols values and its up u in the others. d_out (rows x
+ * cols, contiguous) = silu(g) * u, silu(g) = g / (1 + e^-g), from d_x itself. d_bytes (rows x 2 x
+ * cols) and d_scale (f32[rows][2]): the rows of g and u; both NULL: nothing is saved (serving). */
+int hx_gated_forward(uint32_t format, uint32_t dtype, const void* d_x, uint64_t rows, uint64_t cols,
+                     uint64_t ld, void* d_out, uint8_t* d_bytes, float* d_scale, void* stream);
+
+/* Its backward pass at the saved g and u: d_dx (rows x 2 cols, contiguous) = the gradients of g and
+ * u for d_dout (rows x cols, row stride ld); d_out (rows x cols, or NULL) = silu(g) * u again, for
+ * the weight gradient of the layer behind. */
+int hx_gated_backward(uint32_t format, uint32_t dtype, const void* d_dout, uint64_t ld,
+                      const uint8_t* d_bytes, const float* d_scale, uint64_t rows, uint64_t cols,
+                      void* d_dx, void* d_out, void* stream);
+
+/* Norm of queries and keys for each head, with the position rotation in the same pass, the inputs
+ * saved as 8-bit rows (a row per head of a token). Head h of token t: x, dim values;
+ *   r = (mean(x^2) + eps)^(-1/2);  n = x r w, w = d_wq for the first q_heads heads, d_wk for the
+ *   k_heads behind them;  y = n with the pairs of its first rot_dim values turned by the angles in
+ *   row d_positions[t] of d_cos and d_sin: (a, b) -> (a cos - b sin, b cos + a sin). Pair i is
+ *   (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.
+ * dim: even, 2..512; rot_dim: even, 0..dim. */
+typedef struct {
+  uint32_t format;         /* HX_ROWS_*                                                       */
+  uint32_t dtype;          /* of x and y (dy and dx)                                          */
+  uint32_t weight_dtype;   /* HX_F32 or dtype                                                 */
+  uint32_t position_bits;  /* 32 or 64 (signed)                                               */
+  uint64_t tokens;
+  uint32_t q_heads, k_heads, dim, rot_dim;
+  uint32_t interleaved;
+  float eps;
+  uint64_t places;         /* rows of d_cos and d_sin                                         */
+  const void *d_wq, *d_wk; /* dim values each (unused for 0 heads)                            */
+  const float *d_cos, *d_sin; /* f32[places][rot_dim / 2]                                     */
+  const void* d_positions; /* [tokens]                                                        */
+} hx_head_norm_rope;
+
+/* d_x and d_y are addressed by a token and a head stride (so a packed projection is read in
+ * place); d_y may be d_x with the same strides. d_bytes (tokens x heads x dim) and d_scale
+ * (f32[tokens][heads]): the rows of x; both NULL: nothing is saved. A position outside the tables
+ * raises HX_ERR_ARG in *d_status (NULL: not reported) and makes that token's outputs NaN. */
+int hx_head_norm_rope_forward(const hx_head_norm_rope* p, const void* d_x, uint64_t x_token,
+                              uint64_t x_head, void* d_y, uint64_t y_token, uint64_t y_head,
+                              uint8_t* d_bytes, float* d_scale, uint32_t* d_status, void* stream);
+
+/* The backward pass at the saved x: d_dx, and d_dwq, d_dwk (f32[dim], overwritten; a fixed order of
+ * sums). d_dx may be d_dy with the same strides. d_workspace: hx_head_norm_rope_workspace(dim)
+ * bytes of device memory, clobbered. A position outside the tables makes the weight gradients NaN
+ * too. tokens = 0: the weight gradients are zeros. */
+uint64_t hx_head_norm_rope_workspace(uint32_t dim);
+int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uint64_t dy_token,
+                               uint64_t dy_head, const uint8_t* d_bytes, const float* d_scale,
+                               void* d_dx, uint64_t dx_token, uint64_t dx_head, float* d_dwq,
+                               float* d_dwk, void* d_workspace, uint64_t workspace_bytes,
+                               uint32_t* d_status, void* stream);
+
+/* Weight gradient of a linear layer from the 8-bit rows of its input: d_dw (n_out x n_in, row stride
+ * ld_dw) = dY^T X, plus d_dw's old values if accumulate. d_dy: tokens x n_out (row stride ld_dy), dtype
+ * HX_F16 or HX_BF16; X: d_bytes (tokens x n_in) and d_scale; dw_dtype: HX_F32 or dtype. The products run
+ * on the tensor cores in dtype: X's values are exact there for e4m3 rows in bf16 (and in f16 within its
+ * normal range) and rounded once for INT8 rows; sums are in 32 bits. d_workspace:
+ * hx_weight_grad_workspace(tokens, n_out, n_in) bytes (0: may be NULL), 16-byte aligned, clobbered.
+ * Waits inside the kernel are bounded: HX_ERR_TIMEOUT in *d_status (NULL: not reported). tokens = 0: zeros
+ * (or the old values). n_out <= 2^23, n_in <= 2^22. */
+uint64_t hx_weight_grad_workspace(uint64_t tokens, uint64_t n_out, uint64_t n_in);
+int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy,
+                   const uint8_t* d_bytes, const float* d_scale, uint64_t tokens, uint64_t n_out,
+                   uint64_t n_in, uint32_t dw_dtype, void* d_dw, uint64_t ld_dw, int accumulate,
+                   void* d_workspace, uint64_t workspace_bytes, uint32_t* d_status, void* stream);
+
 /* Measurement helpers (host, fp64). Shannon entropy -sum p log2 p of counts[256] in bits per
  * symbol ("Single-Stage Huffman Encoder for ML Compression", abstract: the ideal the fixed code
  * is compared with), and the mean code length sum count*len / sum count of a codebook (for a

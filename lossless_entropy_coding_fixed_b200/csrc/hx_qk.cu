@@ -1,0 +1,553 @@
+// Per-head RMS norm of queries and keys with the position rotation in the same pass (sm_100a), its
+// inputs kept as 8-bit rows, and the backward pass that reads those rows.
+//
+// Forward, for head h of token t with x = x[t][h], D values:
+//     r = (mean(x^2) + eps)^(-1/2),  n = x r w (w: the queries' or the keys' weight),
+//     y = n with each of its first `rot` values' pairs (a, b) turned by the token's angle:
+//         (a c - b s, b c + a s).
+// Backward at the saved x~: g = dy turned back, dw = sum over heads and tokens of g x~ r,
+//     d = g w,  dx = r (d - x~ r mean(d x~ r)).
+//
+// Both read and write each value once and are bound by memory. A group of L lanes holds one head, 16
+// values per lane, arranged so that both values of a pair are in the same lane (two vectors of PU
+// values each, half the rotated width apart or adjacent): the rotation needs no exchange, the
+// norm one butterfly over L lanes. A group takes up to 8 heads of one token one after another, with
+// the token's cosines and sines and the weight in registers and the next head's loads in flight.
+#include <algorithm>
+#include <cstdint>
+
+#include "hx.h"
+#include "hx_values.h"
+
+namespace {
+
+using namespace hxv;
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 512;       // 32 lanes of 16 values
+constexpr int kMaxBlocks = 1024;   // backward: rows of partial weight gradients in the workspace
+
+struct Args {
+  uint32_t fmt, w_f32;
+  const void* x;       // forward: x; backward: dy
+  uint64_t xt, xh;     // element strides of tokens and heads
+  void* y;             // forward: y; backward: dx
+  uint64_t yt, yh;
+  uint8_t* bytes;      // forward: written or null; backward: read
+  float* scale;
+  uint64_t tokens;
+  uint32_t nq, nk, dim, rot;
+  const void *wq, *wk;
+  const float *cos, *sin;
+  const void* pos;
+  uint32_t pos64;
+  uint64_t places;
+  float eps;
+  uint32_t* status;
+  uint32_t lanes, per;  // lanes per head, heads per item
+  float* part;          // backward: [blocks][dim]
+  uint32_t blocks_q;    // backward: the first blocks take queries, the others keys
+};
+
+// The places of a lane's values: unit j of the lane is vectors of PU values at off0 and off1, whose
+// pairs have the angles `angle` .. angle + PU - 1.
+template <int PU, bool kInter>
+struct Units {
+  uint32_t units, turned, half;
+  __device__ Units(const Args& a)
+      : units(a.dim / (2 * PU)), turned(a.rot / (2 * PU)), half(a.rot / 2) {}
+  __device__ bool has(uint32_t u) const { return u < units; }
+  __device__ bool turns(uint32_t u) const { return u < turned; }
+  __device__ uint32_t off0(uint32_t u) const { return kInter || u >= turned ? 2 * PU * u : PU * u; }
+  __device__ uint32_t off1(uint32_t u) const {
+    return kInter || u >= turned ? 2 * PU * u + PU : half + PU * u;
+  }
+};
+
+// (a, b) -> (a c - b s, b c + a s), pairs across the two vectors or (kInter) inside them.
+template <int PU, bool kInter>
+__device__ __forceinline__ void turn(float (&a)[PU], float (&b)[PU], const float (&c)[PU],
+                                     const float (&s)[PU]) {
+  if constexpr (!kInter) {
+#pragma unroll
+    for (int i = 0; i < PU; ++i) {
+      const float v = a[i] * c[i] - b[i] * s[i];
+      b[i] = b[i] * c[i] + a[i] * s[i];
+      a[i] = v;
+    }
+  } else {
+    // pair i is values 2i, 2i + 1 of the two vectors one after the other
+#pragma unroll
+    for (int i = 0; i < PU; ++i) {
+      float& p = 2 * i < PU ? a[(2 * i) % PU] : b[(2 * i) % PU];
+      float& q = 2 * i + 1 < PU ? a[(2 * i + 1) % PU] : b[(2 * i + 1) % PU];
+      const float v = p * c[i] - q * s[i];
+      q = q * c[i] + p * s[i];
+      p = v;
+    }
+  }
+}
+
+__device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
+  for (uint32_t o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t lanes) {
+  for (uint32_t o = lanes >> 1; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <typename T, int PU, bool kInter>
+__device__ __forceinline__ void load_weight(const Args& a, const void* w, uint32_t sub,
+                                            float (&w0)[8 / PU][PU], float (&w1)[8 / PU][PU]) {
+  const Units<PU, kInter> un(a);
+#pragma unroll
+  for (int j = 0; j < 8 / PU; ++j) {
+    const uint32_t u = j * a.lanes + sub;
+    if (!un.has(u)) {
+#pragma unroll
+      for (int i = 0; i < PU; ++i) w0[j][i] = w1[j][i] = 0.0f;
+    } else if (a.w_f32) {
+      Vec<float, PU> v;
+      v.load(static_cast<const float*>(w) + un.off0(u));
+      v.floats(w0[j]);
+      v.load(static_cast<const float*>(w) + un.off1(u));
+      v.floats(w1[j]);
+    } else {
+      Vec<T, PU> v;
+      v.load(static_cast<const T*>(w) + un.off0(u));
+      v.floats(w0[j]);
+      v.load(static_cast<const T*>(w) + un.off1(u));
+      v.floats(w1[j]);
+    }
+  }
+}
+
+// The token's cosines and sines of the lane's pairs (1 and 0 for values that are not turned).
+// Returns false, and leaves (1, 0), for a position outside the tables.
+template <int PU, bool kInter>
+__device__ __forceinline__ bool load_angles(const Args& a, uint64_t t, uint32_t sub, float sign,
+                                            float (&c)[8 / PU][PU], float (&s)[8 / PU][PU]) {
+  const Units<PU, kInter> un(a);
+  const int64_t p = a.pos64 ? static_cast<const int64_t*>(a.pos)[t]
+                            : (int64_t) static_cast<const int32_t*>(a.pos)[t];
+  const bool ok = p >= 0 && (uint64_t)p < a.places;
+#pragma unroll
+  for (int j = 0; j < 8 / PU; ++j) {
+    const uint32_t u = j * a.lanes + sub;
+    if (ok && un.turns(u)) {
+      const uint64_t at = (uint64_t)p * un.half + PU * u;
+      Vec<float, PU> v;
+      v.load(a.cos + at);
+      v.floats(c[j]);
+      v.load(a.sin + at);
+      v.floats(s[j]);
+#pragma unroll
+      for (int i = 0; i < PU; ++i) s[j][i] *= sign;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PU; ++i) c[j][i] = 1.0f, s[j][i] = 0.0f;
+    }
+  }
+  if (!ok && a.status && sub == 0) atomicOr(a.status, (uint32_t)HX_ERR_ARG);
+  return ok;
+}
+
+template <typename T, int PU, bool kInter>
+__global__ void __launch_bounds__(kThreads) k_qk_forward(const Args a) {
+  constexpr int N = 8 / PU;
+  const Units<PU, kInter> un(a);
+  const uint32_t sub = threadIdx.x % a.lanes, groups = kThreads / a.lanes;
+  const uint64_t item = blockIdx.x * (uint64_t)groups + threadIdx.x / a.lanes;
+  const uint32_t cq = (a.nq + a.per - 1) / a.per, chunks = cq + (a.nk + a.per - 1) / a.per;
+  const bool live = item < a.tokens * chunks;
+  const uint64_t t = live ? item / chunks : 0;
+  const uint32_t ch = live ? (uint32_t)(item - t * chunks) : 0;
+  const bool key = ch >= cq;
+  const uint32_t h0 = key ? a.nq + (ch - cq) * a.per : ch * a.per;
+  const uint32_t h1 = live ? min(h0 + a.per, key ? a.nq + a.nk : a.nq) : h0;
+
+  float w0[N][PU], w1[N][PU], c[N][PU], s[N][PU];
+  Vec<T, PU> v0[N], v1[N];
+  const T* x = static_cast<const T*>(a.x) + t * a.xt;
+  T* y = static_cast<T*>(a.y) + t * a.yt;
+  auto fetch = [&](uint32_t h) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t u = j * a.lanes + sub;
+      if (h < h1 && un.has(u)) {
+        v0[j].load(x + h * a.xh + un.off0(u));
+        v1[j].load(x + h * a.xh + un.off1(u));
+      } else {
+        v0[j].zero();
+        v1[j].zero();
+      }
+    }
+  };
+  fetch(h0);
+  load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w0, w1);
+  const bool ok = load_angles<PU, kInter>(a, t, sub, 1.0f, c, s);
+  for (uint32_t k = 0; k < a.per; ++k) {  // the same count in every lane: the butterflies need all
+    const uint32_t h = h0 + k;
+    float f0[N][PU], f1[N][PU];
+    float sq = 0.0f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v0[j].floats(f0[j]);
+      v1[j].floats(f1[j]);
+      top = v1[j].top(v0[j].top(top));
+#pragma unroll
+      for (int i = 0; i < PU; ++i) sq += f0[j][i] * f0[j][i] + f1[j][i] * f1[j][i];
+    }
+    fetch(h + 1);
+    sq = group_sum(sq, a.lanes);
+    float r = 1.0f / sqrtf(sq / (float)a.dim + a.eps);
+    if (!ok) r = __uint_as_float(0x7fc00000u);
+    if (a.bytes) {
+      top = group_max(top_bits<T>(top), a.lanes);
+      const Scale sc = scale_of<T>(a.fmt, top);
+      if (h < h1) {
+        const uint64_t row = t * (a.nq + a.nk) + h;
+        if (sub == 0) a.scale[row] = sc.s;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint32_t u = j * a.lanes + sub;
+          if (!un.has(u)) continue;
+          to_bytes<PU>(a.fmt, f0[j], sc).store(a.bytes + row * a.dim + un.off0(u));
+          to_bytes<PU>(a.fmt, f1[j], sc).store(a.bytes + row * a.dim + un.off1(u));
+        }
+      }
+    }
+    if (h < h1) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t u = j * a.lanes + sub;
+        if (!un.has(u)) continue;
+#pragma unroll
+        for (int i = 0; i < PU; ++i) {
+          f0[j][i] = f0[j][i] * r * w0[j][i];
+          f1[j][i] = f1[j][i] * r * w1[j][i];
+        }
+        if (un.turns(u)) turn<PU, kInter>(f0[j], f1[j], c[j], s[j]);
+        store<T, PU>(y + h * a.yh + un.off0(u), f0[j]);
+        store<T, PU>(y + h * a.yh + un.off1(u), f1[j]);
+      }
+    }
+  }
+}
+
+template <typename T, int PU, bool kInter>
+__global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const Args a) {
+  constexpr int N = 8 / PU;
+  __shared__ float sums[kThreads * 16];
+  const Units<PU, kInter> un(a);
+  const uint32_t sub = threadIdx.x % a.lanes, groups = kThreads / a.lanes;
+  const uint32_t group = threadIdx.x / a.lanes;
+  const bool key = blockIdx.x >= a.blocks_q;
+  const uint32_t first = key ? a.nq : 0, heads = key ? a.nk : a.nq;
+  const uint32_t chunks = (heads + a.per - 1) / a.per;
+  const uint32_t blocks = key ? gridDim.x - a.blocks_q : a.blocks_q;
+  const uint32_t block = key ? blockIdx.x - a.blocks_q : blockIdx.x;
+  const uint64_t items = a.tokens * chunks;
+
+  float w0[N][PU], w1[N][PU], d0[N][PU], d1[N][PU];
+  load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w0, w1);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < PU; ++i) d0[j][i] = d1[j][i] = 0.0f;
+
+  for (uint64_t base = (uint64_t)block * groups; base < items; base += (uint64_t)blocks * groups) {
+    const uint64_t item = base + group;
+    const bool live = item < items;
+    const uint64_t t = live ? item / chunks : 0;
+    const uint32_t h0 = first + (live ? (uint32_t)(item - t * chunks) : 0) * a.per;
+    const uint32_t h1 = live ? min(h0 + a.per, first + heads) : h0;
+    float c[N][PU], s[N][PU];
+    Vec<T, PU> v0[N], v1[N];
+    Bytes<PU> b0[N], b1[N];
+    float sc = 0.0f;
+    const T* dy = static_cast<const T*>(a.x) + t * a.xt;
+    T* dx = static_cast<T*>(a.y) + t * a.yt;
+    auto fetch = [&](uint32_t h) {
+      const uint64_t row = t * (a.nq + a.nk) + h;
+      sc = h < h1 ? a.scale[row] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t u = j * a.lanes + sub;
+        if (h < h1 && un.has(u)) {
+          v0[j].load(dy + h * a.xh + un.off0(u));
+          v1[j].load(dy + h * a.xh + un.off1(u));
+          b0[j].load(a.bytes + row * a.dim + un.off0(u));
+          b1[j].load(a.bytes + row * a.dim + un.off1(u));
+        } else {
+          v0[j].zero();
+          v1[j].zero();
+#pragma unroll
+          for (int i = 0; i < Bytes<PU>::kRaw; ++i) b0[j].b[i] = b1[j].b[i] = 0;
+        }
+      }
+    };
+    fetch(h0);
+    bool ok = true;
+    if (live) ok = load_angles<PU, kInter>(a, t, sub, -1.0f, c, s);
+    for (uint32_t k = 0; k < a.per; ++k) {
+      const uint32_t h = h0 + k;
+      float g0[N][PU], g1[N][PU], x0[N][PU], x1[N][PU];
+      float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v0[j].floats(g0[j]);
+        v1[j].floats(g1[j]);
+        to_values<PU>(a.fmt, b0[j], sc, x0[j]);
+        to_values<PU>(a.fmt, b1[j], sc, x1[j]);
+      }
+      fetch(h + 1);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t u = j * a.lanes + sub;
+        if (h < h1 && un.turns(u)) turn<PU, kInter>(g0[j], g1[j], c[j], s[j]);
+#pragma unroll
+        for (int i = 0; i < PU; ++i) {
+          sq += x0[j][i] * x0[j][i] + x1[j][i] * x1[j][i];
+          dot += g0[j][i] * w0[j][i] * x0[j][i] + g1[j][i] * w1[j][i] * x1[j][i];
+        }
+      }
+      sq = group_sum(sq, a.lanes);
+      dot = group_sum(dot, a.lanes);
+      float r = 1.0f / sqrtf(sq / (float)a.dim + a.eps);
+      if (!ok) r = __uint_as_float(0x7fc00000u);
+      const float m = dot * r / (float)a.dim;  // mean(d x~ r)
+      if (h < h1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint32_t u = j * a.lanes + sub;
+          if (!un.has(u)) continue;
+#pragma unroll
+          for (int i = 0; i < PU; ++i) {
+            const float n0 = x0[j][i] * r, n1 = x1[j][i] * r;
+            d0[j][i] += g0[j][i] * n0;
+            d1[j][i] += g1[j][i] * n1;
+            g0[j][i] = r * (g0[j][i] * w0[j][i] - n0 * m);
+            g1[j][i] = r * (g1[j][i] * w1[j][i] - n1 * m);
+          }
+          store<T, PU>(dx + h * a.yh + un.off0(u), g0[j]);
+          store<T, PU>(dx + h * a.yh + un.off1(u), g1[j]);
+        }
+      }
+    }
+  }
+
+  // the block's sum of its groups' weight gradients, in the groups' order
+  float* mine = sums + group * (16 * a.lanes);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t u = j * a.lanes + sub;
+    if (!un.has(u)) continue;
+#pragma unroll
+    for (int i = 0; i < PU; ++i) {
+      mine[un.off0(u) + i] = d0[j][i];
+      mine[un.off1(u) + i] = d1[j][i];
+    }
+  }
+  __syncthreads();
+  for (uint32_t d = threadIdx.x; d < a.dim; d += kThreads) {
+    float v = 0.0f;
+    for (uint32_t g = 0; g < groups; ++g) v += sums[g * (16 * a.lanes) + d];
+    a.part[(uint64_t)blockIdx.x * a.dim + d] = v;
+  }
+}
+
+// Sums the blocks' partial weight gradients in a fixed order: 8 interleaved sums per column, then
+// those 8. blockIdx.y: 0 queries, 1 keys.
+__global__ void __launch_bounds__(256) k_qk_weights(const float* __restrict__ part, uint32_t dim,
+                                                    uint32_t blocks_q, uint32_t blocks,
+                                                    float* dwq, float* dwk) {
+  __shared__ float rows[8][32];
+  const uint32_t d = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+  const uint32_t lo = blockIdx.y ? blocks_q : 0, hi = blockIdx.y ? blocks : blocks_q;
+  float* dw = blockIdx.y ? dwk : dwq;
+  float v = 0.0f;
+  if (d < dim)
+    for (uint32_t b = lo + k; b < hi; b += 8) v += part[(uint64_t)b * dim + d];
+  rows[k][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (k == 0 && d < dim && dw) {
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += rows[i][threadIdx.x];
+    dw[d] = v;
+  }
+}
+
+// ------------------------------------------------------------------------------------- launch
+int launched() { return cudaGetLastError() == cudaSuccess ? HX_OK : HX_ERR_CUDA; }
+bool multiple(const void* p, uint64_t of) { return (reinterpret_cast<uintptr_t>(p) % of) == 0; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+// Values per vector: the widest with which every vector of every head starts on its own boundary.
+int vector_of(const Args& a, uint64_t e) {
+  for (int pu = 8; pu > 1; pu /= 2) {
+    const uint64_t al = std::min<uint64_t>(16, pu * e), fl = std::min<uint64_t>(16, pu * 4);
+    const bool strides = (a.xt * e) % al == 0 && (a.xh * e) % al == 0 && (a.yt * e) % al == 0 &&
+                         (a.yh * e) % al == 0;
+    const uint64_t wl = a.w_f32 ? fl : al;
+    if (a.dim % (2 * pu) == 0 && a.rot % (2 * pu) == 0 && strides && multiple(a.x, al) &&
+        multiple(a.y, al) && multiple(a.bytes, pu) && multiple(a.cos, fl) && multiple(a.sin, fl) &&
+        multiple(a.wq, wl) && multiple(a.wk, wl))
+      return pu;
+  }
+  return 1;
+}
+
+template <typename T, int PU, bool kInter>
+int launch(bool backward, const Args& a, uint32_t grid, cudaStream_t s) {
+  if (backward)
+    k_qk_backward<T, PU, kInter><<<grid, kThreads, 0, s>>>(a);
+  else
+    k_qk_forward<T, PU, kInter><<<grid, kThreads, 0, s>>>(a);
+  return launched();
+}
+template <typename T, int PU>
+int launch_style(bool backward, bool inter, const Args& a, uint32_t grid, cudaStream_t s) {
+  return inter ? launch<T, PU, true>(backward, a, grid, s) : launch<T, PU, false>(backward, a, grid, s);
+}
+template <typename T>
+int launch_width(int pu, bool backward, bool inter, const Args& a, uint32_t grid, cudaStream_t s) {
+  switch (pu) {
+    case 8: return launch_style<T, 8>(backward, inter, a, grid, s);
+    case 4: return launch_style<T, 4>(backward, inter, a, grid, s);
+    case 2: return launch_style<T, 2>(backward, inter, a, grid, s);
+    default: return launch_style<T, 1>(backward, inter, a, grid, s);
+  }
+}
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+int check(const Args& a, uint32_t dtype, uint32_t w_dtype, uint32_t pos_bits) {
+  if (a.fmt > HX_ROWS_INT8 || dtype > HX_BF16 || (w_dtype != HX_F32 && w_dtype != dtype) ||
+      (pos_bits != 32 && pos_bits != 64))
+    return HX_ERR_ARG;
+  if (a.dim < 2 || a.dim > kMaxDim || a.dim % 2 || a.rot > a.dim || a.rot % 2) return HX_ERR_ARG;
+  const uint64_t heads = (uint64_t)a.nq + a.nk;
+  if (!heads || heads > (1u << 20) || a.tokens >= (1ull << 31) || !(a.eps >= 0.0f) ||
+      a.places >= (1ull << 40))
+    return HX_ERR_ARG;
+  if (a.tokens && a.tokens * heads > (1ull << 40) / a.dim) return HX_ERR_ARG;
+  if (a.tokens && ((a.nq && !a.wq) || (a.nk && !a.wk))) return HX_ERR_ARG;
+  if (a.tokens && (!a.x || !a.y || !a.pos || !a.places || (a.rot && (!a.cos || !a.sin)))) return HX_ERR_ARG;
+  const uint64_t e = dtype == HX_F32 ? 4 : 2, we = w_dtype == HX_F32 ? 4 : 2;
+  if (!multiple(a.x, e) || !multiple(a.y, e) || !multiple(a.wq, we) || !multiple(a.wk, we) ||
+      !multiple(a.cos, 4) || !multiple(a.sin, 4) || !multiple(a.scale, 4) ||
+      !multiple(a.pos, pos_bits / 8) || !multiple(a.status, 4))
+    return HX_ERR_ARG;
+  return HX_OK;
+}
+
+// The lanes per head: a power of two with 16 values each. Heads per item: 8, so that a token's
+// angles and the weight are loaded once for them, halved while the items would not fill the GPU.
+void arrange(Args* a, int pu, int sms) {
+  uint32_t lanes = 1;
+  while (lanes * 16 < a->dim) lanes *= 2;
+  (void)pu;
+  a->lanes = lanes;
+  a->per = 8;
+  const uint64_t want = (uint64_t)sms * (1024 / lanes);
+  while (a->per > 1 && a->tokens * (ceil_div(a->nq, a->per) + ceil_div(a->nk, a->per)) < want)
+    a->per /= 2;
+}
+
+int run(bool backward, uint32_t dtype, int pu, uint32_t style, const Args& a, uint64_t grid,
+        cudaStream_t s) {
+  if (grid >= (1ull << 31)) return HX_ERR_ARG;
+  if (dtype == HX_F32) return launch_width<float>(pu, backward, style, a, (uint32_t)grid, s);
+  if (dtype == HX_F16) return launch_width<__half>(pu, backward, style, a, (uint32_t)grid, s);
+  return launch_width<__nv_bfloat16>(pu, backward, style, a, (uint32_t)grid, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int hx_head_norm_rope_forward(const hx_head_norm_rope* p, const void* d_x, uint64_t x_token,
+                              uint64_t x_head, void* d_y, uint64_t y_token, uint64_t y_head,
+                              uint8_t* d_bytes, float* d_scale, uint32_t* d_status, void* stream) {
+  if (!p || !d_bytes != !d_scale) return HX_ERR_ARG;
+  Args a{};
+  a.fmt = p->format, a.w_f32 = p->weight_dtype == HX_F32;
+  a.x = d_x, a.xt = x_token, a.xh = x_head, a.y = d_y, a.yt = y_token, a.yh = y_head;
+  a.bytes = d_bytes, a.scale = d_scale, a.tokens = p->tokens;
+  a.nq = p->q_heads, a.nk = p->k_heads, a.dim = p->dim, a.rot = p->rot_dim;
+  a.wq = p->d_wq, a.wk = p->d_wk, a.cos = p->d_cos, a.sin = p->d_sin;
+  a.pos = p->d_positions, a.pos64 = p->position_bits == 64, a.places = p->places;
+  a.eps = p->eps, a.status = d_status;
+  if (const int rc = check(a, p->dtype, p->weight_dtype, p->position_bits)) return rc;
+  if (!a.tokens) return HX_OK;
+  const int sms = sm_count();
+  if (!sms) return HX_ERR_CUDA;
+  const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2);
+  arrange(&a, pu, sms);
+  const uint64_t items = a.tokens * (ceil_div(a.nq, a.per) + ceil_div(a.nk, a.per));
+  return run(false, p->dtype, pu, p->interleaved != 0, a, ceil_div(items, kThreads / a.lanes),
+             static_cast<cudaStream_t>(stream));
+}
+
+uint64_t hx_head_norm_rope_workspace(uint32_t dim) { return (uint64_t)kMaxBlocks * dim * 4; }
+
+int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uint64_t dy_token,
+                               uint64_t dy_head, const uint8_t* d_bytes, const float* d_scale,
+                               void* d_dx, uint64_t dx_token, uint64_t dx_head, float* d_dwq,
+                               float* d_dwk, void* d_workspace, uint64_t workspace_bytes,
+                               uint32_t* d_status, void* stream) {
+  if (!p) return HX_ERR_ARG;
+  Args a{};
+  a.fmt = p->format, a.w_f32 = p->weight_dtype == HX_F32;
+  a.x = d_dy, a.xt = dy_token, a.xh = dy_head, a.y = d_dx, a.yt = dx_token, a.yh = dx_head;
+  a.bytes = const_cast<uint8_t*>(d_bytes), a.scale = const_cast<float*>(d_scale);
+  a.tokens = p->tokens;
+  a.nq = p->q_heads, a.nk = p->k_heads, a.dim = p->dim, a.rot = p->rot_dim;
+  a.wq = p->d_wq, a.wk = p->d_wk, a.cos = p->d_cos, a.sin = p->d_sin;
+  a.pos = p->d_positions, a.pos64 = p->position_bits == 64, a.places = p->places;
+  a.eps = p->eps, a.status = d_status;
+  if (const int rc = check(a, p->dtype, p->weight_dtype, p->position_bits)) return rc;
+  if ((a.nq && !d_dwq) || (a.nk && !d_dwk) || !multiple(d_dwq, 4) || !multiple(d_dwk, 4)) return HX_ERR_ARG;
+  if (!d_workspace || !multiple(d_workspace, 4) ||
+      workspace_bytes < hx_head_norm_rope_workspace(a.dim))
+    return HX_ERR_ARG;
+  if (a.tokens && (!d_bytes || !d_scale)) return HX_ERR_ARG;
+  const int sms = sm_count();
+  if (!sms) return HX_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.part = static_cast<float*>(d_workspace);
+  uint64_t blocks = 0;
+  if (a.tokens) {
+    const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2);
+    arrange(&a, pu, sms);
+    // two blocks per SM hold all groups that fit at once; queries and keys share them by heads
+    const uint64_t groups = kThreads / a.lanes;
+    const uint64_t bq = ceil_div(a.tokens * ceil_div(a.nq, a.per), groups);
+    const uint64_t bk = ceil_div(a.tokens * ceil_div(a.nk, a.per), groups);
+    const uint64_t most = std::min<uint64_t>(kMaxBlocks, 2 * (uint64_t)sms);
+    uint64_t q = bq, k = bk;
+    if (bq + bk > most) {
+      q = bq ? std::max<uint64_t>(1, most * bq / (bq + bk)) : 0;
+      if (bk && q == most) --q;
+      k = bk ? most - q : 0;
+    }
+    a.blocks_q = (uint32_t)q;
+    blocks = q + k;
+    if (const int rc = run(true, p->dtype, pu, p->interleaved != 0, a, blocks, s)) return rc;
+  }
+  k_qk_weights<<<dim3((a.dim + 31) / 32, 2), 256, 0, s>>>(a.part, a.dim, a.blocks_q, (uint32_t)blocks,
+                                                        d_dwq, d_dwk);
+  return launched();
+}
+
+}  // extern "C"

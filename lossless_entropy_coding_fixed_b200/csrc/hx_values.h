@@ -1,0 +1,285 @@
+// Device helpers of the 8-bit-row kernels (private to the library): element types, the scale and
+// byte of a value, and loads and stores of W consecutive elements.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hx.h"
+
+namespace hxv {
+
+// ------------------------------------------------------------------------------ element types
+template <typename T>
+struct Type;
+template <>
+struct Type<float> {
+  static constexpr uint32_t kInf = 0x7f800000u;
+  static __device__ float from_bits(uint32_t b) { return __uint_as_float(b); }
+  static __device__ float to_f(float v) { return v; }
+  static __device__ float from_f(float v) { return v; }
+};
+template <>
+struct Type<__half> {
+  static constexpr uint32_t kInf = 0x7c00u;
+  static __device__ float from_bits(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+  static __device__ float to_f(__half v) { return __half2float(v); }
+  static __device__ __half from_f(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Type<__nv_bfloat16> {
+  static constexpr uint32_t kInf = 0x7f80u;
+  static __device__ float from_bits(uint32_t b) { return __uint_as_float(b << 16); }
+  static __device__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+};
+
+// Two 16-bit elements of a word as floats, and back.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// --------------------------------------------------------------------- W consecutive elements
+// Loaded as they are in memory: 8 or 4 elements of 32 bits, 8, 4 or 2 of 16 bits, or 1 of either. The address is a
+// multiple of min(16, W * sizeof(T)). kRaw: 32-bit registers held.
+template <typename T, int W>
+struct Vec {
+  static constexpr int kRaw = W * sizeof(T) < 4 ? 1 : W * sizeof(T) / 4;
+  uint32_t r[kRaw];
+
+  __device__ __forceinline__ void load(const T* p) {
+    constexpr int kBytes = W * sizeof(T);
+    if constexpr (kBytes == 32) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p), b = *(reinterpret_cast<const uint4*>(p) + 1);
+      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+      r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    } else if constexpr (kBytes == 16) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      r[0] = a.x, r[1] = a.y;
+    } else if constexpr (kBytes == 4) {
+      r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      r[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) r[i] = 0;
+  }
+  // bits of the largest magnitude so far (as T's bits; NaN and infinities compare above all
+  // finite values), per 16-bit half for 16-bit types
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) {
+      if constexpr (sizeof(T) == 4)
+        m = max(m, r[i] & 0x7fffffffu);
+      else
+        m = __vmaxu2(m, r[i] & 0x7fff7fffu);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void floats(float (&f)[W]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[i] = __uint_as_float(r[i]);
+    } else if constexpr (W == 1) {
+      f[0] = unpack2<T>(r[0]).x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const float2 v = unpack2<T>(r[i]);
+        f[2 * i] = v.x, f[2 * i + 1] = v.y;
+      }
+    }
+  }
+};
+
+// One word's worth of top() (both halves of a 16-bit type) as the bits of one element.
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return m;
+  return max(m & 0xffffu, m >> 16);
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store(T* p, const float (&f)[W]) {
+  if constexpr (W == 1) {
+    *p = Type<T>::from_f(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    if constexpr (W == 2) {
+      *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+  } else {
+    uint32_t r[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) r[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    if constexpr (W == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+    else if constexpr (W == 4)
+      *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = r[0];
+  }
+}
+
+// W bytes, lowest address in the low byte of b[0]; the address is a multiple of W.
+template <int W>
+struct Bytes {
+  static constexpr int kRaw = W < 4 ? 1 : W / 4;
+  uint32_t b[kRaw];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (W == 8) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      b[0] = a.x, b[1] = a.y;
+    } else if constexpr (W == 4) {
+      b[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (W == 2) {
+      b[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+      b[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
+    if constexpr (W == 8)
+      *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+    else if constexpr (W == 4)
+      *reinterpret_cast<uint32_t*>(p) = b[0];
+    else if constexpr (W == 2)
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)b[0];
+    else
+      *p = (uint8_t)b[0];
+  }
+};
+
+// ------------------------------------------------------------------------- scales and bytes
+// A row's scale from the bits of its largest magnitude, and the factor that a value is multiplied
+// by on its way to a byte. A row with a NaN or an infinity has scale NaN and factor 0 (its bytes
+// are cleared by the caller).
+struct Scale {
+  float s, inv;
+  bool fine;
+};
+template <typename T>
+__device__ __forceinline__ Scale scale_of(uint32_t fmt, uint32_t bits) {
+  Scale r;
+  r.fine = bits < Type<T>::kInf;
+  const float top = Type<T>::from_bits(bits);
+  if (fmt == HX_ROWS_E4M3) {
+    // The smallest power of two with top / s <= 448 = 1.75 * 2^8: a scale that changes no
+    // mantissa, so a byte times its scale is exact in every type and the bytes' distribution
+    // over e4m3's fraction bits is the values' own. top = f 2^E: s = 2^(E-8), doubled if f > 1.75.
+    const uint32_t b = __float_as_uint(top);
+    int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
+    e = min(max(e, 1), 246);  // 2^-126 .. 2^119: 448 s stays finite
+    r.s = __uint_as_float((uint32_t)e << 23);
+    r.inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  } else {
+    // Symmetric INT8; 127 s stays finite at s <= 2^121.
+    r.s = fminf(fmaxf(__fdiv_rn(top, 127.0f), 0x1p-126f), 0x1p121f);
+    r.inv = __frcp_rn(r.s);
+  }
+  if (top == 0.0f) r.s = r.inv = 1.0f;
+  if (!r.fine) r.s = __uint_as_float(0x7fc00000u), r.inv = 0.0f;
+  return r;
+}
+
+// W values to bytes. INT8 is the nearest integer (ties to even) of the 32-bit quotient x / s. x * inv
+// is within 2^-15 of that quotient (|x / s| <= 128; inv, the product and the quotient each round
+// once, 3 * 2^-24 * 128 < 2^-15), so it rounds to the same integer unless it lies within 2^-14 of
+// a half: then the division itself decides. Adding 1.5 * 2^23 leaves that integer in the low byte.
+template <int W>
+__device__ __forceinline__ Bytes<W> to_bytes(uint32_t fmt, const float (&x)[W], const Scale& sc) {
+  Bytes<W> out;
+  if (fmt == HX_ROWS_E4M3) {
+    uint32_t h[(W + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < (W + 1) / 2; ++i) {
+      const float hi = 2 * i + 1 < W ? x[(2 * i + 1) % W] * sc.inv : 0.0f;
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * sc.inv, hi), __NV_SATFINITE, __NV_E4M3);
+    }
+#pragma unroll
+    for (int i = 0; i < Bytes<W>::kRaw; ++i) out.b[i] = W >= 4 ? h[(2 * i) % ((W + 1) / 2)] | h[(2 * i + 1) % ((W + 1) / 2)] << 16 : h[i];
+  } else {
+    constexpr float kRound = 12582912.0f;
+    uint32_t q[W];
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float t = fminf(fmaxf(x[i] * sc.inv, -127.0f), 127.0f);
+      const float r = __fadd_rn(t, kRound);
+      q[i] = __float_as_uint(r);
+      near |= fabsf(t - __fsub_rn(r, kRound)) > 0.5f - 0x1p-14f;
+    }
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        q[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(x[i], sc.s), -127.0f), 127.0f), kRound));
+    }
+#pragma unroll
+    for (int i = 0; i < Bytes<W>::kRaw; ++i) {
+      if constexpr (W >= 4)
+        out.b[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
+      else if constexpr (W == 2)
+        out.b[i] = __byte_perm(q[0], q[1], 0x0040);
+      else
+        out.b[i] = q[0] & 0xffu;
+    }
+  }
+  if (!sc.fine) {
+#pragma unroll
+    for (int i = 0; i < Bytes<W>::kRaw; ++i) out.b[i] = 0;
+  }
+  return out;
+}
+
+// W bytes back to values: byte value times scale, one rounding to 32 bits (none for e4m3).
+template <int W>
+__device__ __forceinline__ void to_values(uint32_t fmt, const Bytes<W>& in, float s, float (&x)[W]) {
+  if (fmt == HX_ROWS_E4M3) {
+#pragma unroll
+    for (int i = 0; i < (W + 1) / 2; ++i) {
+      const uint32_t two = in.b[i / 2] >> (16 * (i & 1));
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      x[2 * i] = v.x * s;
+      if (2 * i + 1 < W) x[(2 * i + 1) % W] = v.y * s;
+    }
+  } else {
+    // 2^23 + (byte + 128) from its bits (an integer conversion runs at a quarter of this rate)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t f = __byte_perm(in.b[i / 4] ^ 0x80808080u, 0x4b000000u, 0x7650u | (i & 3));
+      x[i] = __fsub_rn(__uint_as_float(f), 8388736.0f) * s;
+    }
+  }
+}
+
+}  // namespace hxv

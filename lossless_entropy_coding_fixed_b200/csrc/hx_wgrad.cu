@@ -1,0 +1,550 @@
+// Weight gradient of a linear layer from the 8-bit rows of its input (sm_100a):
+//     dW[o][i] = sum over tokens t of dY[t][o] * s_t * q[t][i].
+//
+// A product of two matrices whose contraction runs over the tokens, so both operands are stored with
+// the contraction outermost (MN-major). Tensor cores: tcgen05.mma, accumulators in TMEM, one CTA
+// per tile of BM output by BN input features, steps of 64 tokens.
+//   warps 0-7   read the bytes (8 columns of a token per lane, the next steps' already in flight),
+//               turn them into s_t q in dY's type and write them to shared memory in the 128-byte
+//               swizzle that the tensor core reads; at the end they read TMEM and store the tile.
+//   warp 8      brings dY's tile by TMA, in the same swizzle.
+//   warp 9      issues the products.
+// The bytes never exist as a 16-bit matrix in memory. s_t q in bf16 is exact for e4m3 (the scale is a
+// power of two); for INT8 it rounds once, by at most half a step of dY's own type. Sums are the tensor
+// core's 32-bit accumulators.
+//
+// Few tiles: the tokens are split over several CTAs per tile, whose 32-bit partial tiles a second
+// kernel adds in order.
+//
+// Every wait is bounded (2 s); when one runs out the CTA raises HX_ERR_TIMEOUT, waits for its own
+// copies in flight, frees its TMEM and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "hx.h"
+#include "hx_values.h"
+
+namespace {
+
+using namespace hxv;
+
+constexpr int kStep = 64;             // tokens per pipeline stage
+constexpr int kConvert = 256;         // converting threads (warps 0-7)
+constexpr int kThreads = kConvert + 64;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMaxSplits = 32;
+
+struct Args {
+  uint32_t fmt;
+  const void* dy;  // only without TMA
+  uint64_t ld_dy;
+  const uint8_t* bytes;
+  const float* scale;
+  uint64_t tokens;
+  uint32_t n_out, n_in;
+  void* dw;
+  uint64_t ld_dw;
+  uint32_t dw_dtype, accumulate, dw_wide, x_wide;
+  float* part;         // with splits > 1: [split][n_out][n_in]
+  uint32_t splits, steps;
+  uint32_t* status;
+};
+
+// ------------------------------------------------------------------------------------ barriers
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of `parity` to complete. False once this wait, or any other of the CTA, ran out.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(bar, parity)) return true;
+    if (*failed) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *failed = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, failed);
+}
+
+// --------------------------------------------------------------------------------- tensor core
+// Shared memory operand, MN-major with 128-byte swizzle: blocks of 64 values of M or N by 64 tokens, a
+// token's 64 values in one 128-byte line; 8 lines per swizzle atom (stride 1024), blocks 8192 apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  constexpr uint64_t kBlock = 8192 >> 4, kAtom = 1024 >> 4;
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | kBlock << 16 | kAtom << 32 | 1ull << 46 | 2ull << 61;
+}
+template <typename T, int N>
+__device__ constexpr uint32_t instruction() {
+  constexpr uint32_t type = sizeof(T) && Type<T>::kInf == 0x7f80u ? 1 : 0;  // bf16 or f16
+  return 1u << 4 | type << 7 | type << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+      "%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+template <int MT, int NT>
+struct Tile {
+  static constexpr int BM = 128 * MT, BN = NT;
+  static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;
+  static constexpr int kStages = 196608 / (kA + kB);
+  static constexpr int kCols = MT * NT;  // TMEM columns: a power of two of at least 32
+  static constexpr int kSmem = kStages * (kA + kB) + 1024;
+  static_assert(kStages >= 2 && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
+};
+
+struct Barriers {
+  uint64_t copied[8], converted[8], empty[8], done;
+  uint32_t tmem, failed;
+};
+
+// ---------------------------------------------------------------------------------- conversion
+// 8 bytes of one token, columns c .. c + 7 (zeros behind the last token or column).
+__device__ __forceinline__ Bytes<8> fetch_bytes(const Args& a, uint64_t t, uint32_t c) {
+  Bytes<8> b;
+  b.b[0] = b.b[1] = 0;
+  if (t >= a.tokens || c >= a.n_in) return b;
+  const uint8_t* p = a.bytes + t * a.n_in + c;
+  if (a.x_wide) {
+    b.load(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < a.n_in) b.b[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+  }
+  return b;
+}
+
+// 8 values of dY without TMA.
+template <typename T>
+__device__ __forceinline__ uint4 fetch_dy(const Args& a, uint64_t t, uint32_t c) {
+  uint32_t r[4] = {0, 0, 0, 0};
+  if (t < a.tokens) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.dy) + t * a.ld_dy + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < a.n_out) r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 convert(uint32_t fmt, const Bytes<8>& b, float s) {
+  float f[8];
+  to_values<8>(fmt, b, s, f);
+  if constexpr (Type<T>::kInf == 0x7c00u) {
+    // a row near fp16's largest value can round above it in its byte
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] > 65504.0f ? 65504.0f : f[i] < -65504.0f ? -65504.0f : f[i];
+  }
+  return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+}
+
+__device__ __forceinline__ void put(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// ------------------------------------------------------------------------------------ the tile
+template <typename O>
+__device__ __forceinline__ void store_tile(const Args& a, uint32_t row, uint32_t col, const uint32_t (&r)[32]) {
+  O* o = static_cast<O*>(a.dw) + (uint64_t)row * a.ld_dw + col;
+  if (a.dw_wide && col + 32 <= a.n_in) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[i + j]);
+      if (a.accumulate) {
+        Vec<O, 8> old;
+        old.load(o + i);
+        float g[8];
+        old.floats(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+      }
+      store<O, 8>(o + i, f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < a.n_in) {
+        float f = __uint_as_float(r[i]);
+        if (a.accumulate) f += Type<O>::to_f(o[i]);
+        o[i] = Type<O>::from_f(f);
+      }
+  }
+}
+
+template <typename T, int MT, int NT, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap map, const Args a) {
+  using S = Tile<MT, NT>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Barriers bars;
+  const uint32_t tiles = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t m0 = blockIdx.x * S::BM, n0 = blockIdx.y * S::BN, split = blockIdx.z;
+  const uint32_t per = (a.steps + a.splits - 1) / a.splits;
+  const uint32_t k0 = min(split * per, a.steps), k1 = min(k0 + per, a.steps), steps = k1 - k0;
+  volatile uint32_t* failed = &bars.failed;
+  auto copied = [&](uint32_t s) { return smem_addr(&bars.copied[s]); };
+  auto converted = [&](uint32_t s) { return smem_addr(&bars.converted[s]); };
+  auto empty = [&](uint32_t s) { return smem_addr(&bars.empty[s]); };
+  const uint32_t done = smem_addr(&bars.done);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      bar_init(copied(s), 1);
+      bar_init(converted(s), kConvert / 32);
+      bar_init(empty(s), 1);
+    }
+    bar_init(done, 1);
+    bars.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
+                 "r"((uint32_t)S::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+
+  if (warp < 8) {
+    // ---- converting warps: tokens 8 warp .. 8 warp + 7 of every step
+    // 8 columns per lane: a warp's load is one token's 256 columns, or two tokens' 128 (lanes
+    // 16-31 the odd one). Lanes 8 i .. 8 i + 7 write one whole line, so no two share a bank.
+    static_assert(NT == 256 || NT == 128, "");
+    constexpr int kLoads = NT == 256 ? 8 : 4;
+    Bytes<8> b[2][kLoads];
+    float sc[2];
+    auto token_of = [&](int j) { return NT == 256 ? j : 2 * j + (int)(lane >> 4); };
+    auto fetch = [&](uint32_t k, int buf) {
+      const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * 8;
+      const uint32_t c = n0 + (NT == 256 ? lane : lane & 15) * 8;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) b[buf][j] = fetch_bytes(a, k < steps ? t + token_of(j) : a.tokens, c);
+      sc[buf] = 0.0f;
+      if (k < steps && t + (lane & 7) < a.tokens) sc[buf] = a.scale[t + (lane & 7)];
+    };
+    auto one = [&](uint32_t k, int buf) {
+      const uint32_t s = k % S::kStages;
+      // one answer per warp: what follows is for whole warps
+      if (!__all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed))) return false;
+      const uint32_t A = tiles + s * (S::kA + S::kB), B = A + S::kA;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int tk = token_of(j);
+        const float f = __shfl_sync(0xffffffffu, sc[buf], tk);
+        const uint32_t ch = NT == 256 ? lane : lane & 15;
+        put(B + (ch >> 3) * 8192 + (warp * 8 + tk) * 128 + (((ch & 7) ^ tk) << 4), convert<T>(a.fmt, b[buf][j], f));
+      }
+      if constexpr (!kTma) {
+        const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * 8;
+        for (int h = 0; h < S::BM; h += 256)
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t ch = h / 8 + lane;
+            if (ch * 8 < S::BM)
+              put(A + (ch >> 3) * 8192 + (warp * 8 + j) * 128 + (((ch & 7) ^ j) << 4), fetch_dy<T>(a, t + j, m0 + ch * 8));
+          }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(converted(s));
+      return true;
+    };
+    fetch(0, 0);
+    fetch(1, 1);
+    bool ok = true;
+    for (uint32_t k = 0; k < steps; k += 2) {
+      if (!(ok = one(k, 0))) break;
+      fetch(k + 2, 0);
+      if (k + 1 >= steps) break;
+      if (!(ok = one(k + 1, 1))) break;
+      fetch(k + 3, 1);
+    }
+    // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
+    if (ok && steps) ok = bar_wait(done, 0, failed);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (__all_sync(0xffffffffu, ok)) {
+      const uint32_t mt = MT == 2 ? warp >> 2 : 0;
+      const uint32_t c0 = MT == 2 ? 0 : (warp >> 2) * (NT / 2), c1 = MT == 2 ? NT : c0 + NT / 2;
+      const uint32_t row = m0 + mt * 128 + (warp & 3) * 32 + lane;
+      for (uint32_t c = c0; c < c1; c += 32) {
+        uint32_t r[32];
+        if (steps) {
+          tmem_load32(tmem + ((warp & 3) * 32 << 16) + mt * NT + c, r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0;
+        }
+        if (row >= a.n_out || n0 + c >= a.n_in) {
+          // nothing of the matrix here
+        } else if (a.splits > 1) {
+          Args p = a;
+          p.dw = a.part + (uint64_t)split * a.n_out * a.n_in;
+          p.ld_dw = a.n_in;
+          p.accumulate = 0;
+          p.dw_wide = a.n_in % 4 == 0;
+          store_tile<float>(p, row, n0 + c, r);
+        } else if (a.dw_dtype == HX_F32) {
+          store_tile<float>(a, row, n0 + c, r);
+        } else {
+          store_tile<T>(a, row, n0 + c, r);
+        }
+        __syncwarp();
+      }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  } else if (warp == 8) {
+    if (kTma && lane == 0) {
+      uint32_t k = 0;
+      for (; k < steps; ++k) {
+        const uint32_t s = k % S::kStages;
+        if (!bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)) break;
+        bar_expect(copied(s), S::kA);
+        const int32_t t = (int32_t)((k0 + k) * kStep);
+        for (int i = 0; i < S::BM / 64; ++i)
+          asm volatile(
+              "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                  tiles + s * (S::kA + S::kB) + i * 8192),
+              "l"(&map), "r"((int32_t)(m0 + i * 64)), "r"(t), "r"(copied(s))
+              : "memory");
+      }
+      if (k < steps) {  // gave up: wait for the copies already on their way
+        const uint64_t t0 = now_ns();
+        for (uint32_t i = k > S::kStages ? k - S::kStages : 0; i < k; ++i)
+          while (!bar_try(copied(i % S::kStages), (i / S::kStages) & 1) && now_ns() - t0 < kWaitNs) {
+          }
+      }
+    }
+  } else if (lane == 0) {
+    bool ok = true;
+    for (uint32_t k = 0; k < steps; ++k) {
+      const uint32_t s = k % S::kStages, parity = (k / S::kStages) & 1;
+      if (!(ok = bar_wait(converted(s), parity, failed) && (!kTma || bar_wait(copied(s), parity, failed)))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t A = tiles + s * (S::kA + S::kB), B = A + S::kA;
+#pragma unroll
+      for (int kk = 0; kk < kStep / 16; ++kk)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          mma(tmem + mt * NT, operand(A + mt * 16384 + kk * 2048), operand(B + kk * 2048), instruction<T, NT>(),
+              k > 0 || kk > 0);
+      commit(empty(s));
+    }
+    // the products issued so far end before the TMEM is freed, also when a wait ran out
+    commit(done);
+    if (!ok) {
+      const uint64_t t0 = now_ns();
+      while (!bar_try(done, 0) && now_ns() - t0 < kWaitNs) {
+      }
+      if (a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
+  if (warp == 9) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kCols));
+  }
+}
+
+// dW = (old dW if accumulate) + the splits' partial sums, in their order.
+template <typename O>
+__global__ void __launch_bounds__(256)
+    k_wgrad_join(const float* __restrict__ part, uint32_t splits, uint32_t n_out, uint32_t n_in, O* dw,
+                 uint64_t ld, uint32_t accumulate) {
+  const uint64_t all = (uint64_t)n_out * n_in;
+  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
+    const uint64_t row = i >> 32 ? i / n_in : (uint32_t)i / n_in;
+    O* o = dw + row * ld + (i - row * n_in);
+    float v = accumulate ? Type<O>::to_f(*o) : 0.0f, sum = 0.0f;
+    for (uint32_t s = 0; s < splits; ++s) sum += part[s * all + i];
+    *o = Type<O>::from_f(v + sum);
+  }
+}
+
+// ------------------------------------------------------------------------------------- launch
+int launched() { return cudaGetLastError() == cudaSuccess ? HX_OK : HX_ERR_CUDA; }
+bool multiple(const void* p, uint64_t of) { return (reinterpret_cast<uintptr_t>(p) % of) == 0; }
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+template <typename T, int MT, int NT, bool kTma>
+int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  using S = Tile<MT, NT>;
+  if (cudaFuncSetAttribute(k_wgrad<T, MT, NT, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+    return HX_ERR_CUDA;
+  const dim3 grid((a.n_out + S::BM - 1) / S::BM, (a.n_in + S::BN - 1) / S::BN, a.splits);
+  k_wgrad<T, MT, NT, kTma><<<grid, kThreads, S::kSmem, s>>>(map, a);
+  return launched();
+}
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  bool big;
+  uint32_t splits;
+};
+
+// Tiles of 256 x 256 once they fill the GPU (148 SMs), else of 128 x 128; tokens split so that the
+// CTAs fill it once, at least 4 steps of 64 tokens each.
+Plan plan(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+  Plan p{};
+  constexpr uint64_t kSms = 148;
+  const uint64_t steps = ceil_div(tokens, kStep);
+  p.big = ceil_div(n_out, 256) * ceil_div(n_in, 256) >= kSms;
+  const uint64_t tiles = p.big ? ceil_div(n_out, 256) * ceil_div(n_in, 256) : ceil_div(n_out, 128) * ceil_div(n_in, 128);
+  uint64_t splits = tiles < kSms ? std::min<uint64_t>(kSms / tiles, steps / 4) : 1;
+  splits = std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
+  // no empty splits: every one has ceil(steps / splits) steps but the last
+  if (steps) splits = ceil_div(steps, ceil_div(steps, splits));
+  p.splits = (uint32_t)splits;
+  return p;
+}
+
+template <typename T>
+int run(const Plan& p, bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  int rc;
+  if (p.big)
+    rc = tma ? launch<T, 2, 256, true>(map, a, s) : launch<T, 2, 256, false>(map, a, s);
+  else
+    rc = tma ? launch<T, 1, 128, true>(map, a, s) : launch<T, 1, 128, false>(map, a, s);
+  if (rc || a.splits == 1) return rc;
+  const uint32_t grid = (uint32_t)std::min<uint64_t>(148 * 8, ceil_div((uint64_t)a.n_out * a.n_in, 256));
+  if (a.dw_dtype == HX_F32)
+    k_wgrad_join<float><<<grid, 256, 0, s>>>(a.part, a.splits, a.n_out, a.n_in, static_cast<float*>(a.dw), a.ld_dw, a.accumulate);
+  else
+    k_wgrad_join<T><<<grid, 256, 0, s>>>(a.part, a.splits, a.n_out, a.n_in, static_cast<T*>(a.dw), a.ld_dw, a.accumulate);
+  return launched();
+}
+
+bool bad_sizes(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+  return tokens >= (1ull << 31) - 64 || !n_out || !n_in || n_out > (1ull << 23) || n_in > (1ull << 22);
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t hx_weight_grad_workspace(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+  if (bad_sizes(tokens, n_out, n_in)) return 0;
+  const Plan p = plan(tokens, n_out, n_in);
+  return p.splits > 1 ? p.splits * n_out * n_in * 4 : 0;
+}
+
+int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes,
+                   const float* d_scale, uint64_t tokens, uint64_t n_out, uint64_t n_in, uint32_t dw_dtype,
+                   void* d_dw, uint64_t ld_dw, int accumulate, void* d_workspace, uint64_t workspace_bytes,
+                   uint32_t* d_status, void* stream) {
+  if (format > HX_ROWS_INT8 || (dtype != HX_F16 && dtype != HX_BF16) || (dw_dtype != HX_F32 && dw_dtype != dtype))
+    return HX_ERR_ARG;
+  if (bad_sizes(tokens, n_out, n_in) || (tokens > 1 && ld_dy < n_out) || (n_out > 1 && ld_dw < n_in)) return HX_ERR_ARG;
+  if (!d_dw || !multiple(d_dw, dw_dtype == HX_F32 ? 4 : 2) || !multiple(d_status, 4)) return HX_ERR_ARG;
+  if (tokens && (!d_dy || !d_bytes || !d_scale || !multiple(d_dy, 2) || !multiple(d_scale, 4))) return HX_ERR_ARG;
+  if (!tokens && accumulate) return HX_OK;
+  const Plan p = plan(tokens, n_out, n_in);
+  if (p.splits > 1 && (!d_workspace || !multiple(d_workspace, 16) ||
+                       workspace_bytes < hx_weight_grad_workspace(tokens, n_out, n_in)))
+    return HX_ERR_ARG;
+  Args a{};
+  a.fmt = format, a.dy = d_dy, a.ld_dy = ld_dy, a.bytes = d_bytes, a.scale = d_scale;
+  a.tokens = tokens, a.n_out = (uint32_t)n_out, a.n_in = (uint32_t)n_in;
+  a.dw = d_dw, a.ld_dw = ld_dw, a.dw_dtype = dw_dtype, a.accumulate = accumulate != 0;
+  a.dw_wide = multiple(d_dw, 16) && (n_out == 1 || ld_dw * (dw_dtype == HX_F32 ? 4 : 2) % 16 == 0);
+  a.x_wide = n_in % 8 == 0 && multiple(d_bytes, 8);
+  a.part = static_cast<float*>(d_workspace), a.splits = p.splits;
+  a.steps = (uint32_t)ceil_div(tokens, kStep), a.status = d_status;
+  // TMA wants rows that start on 16 bytes
+  const uint64_t pitch = tokens > 1 ? ld_dy * 2 : (n_out * 2 + 15) / 16 * 16;
+  const bool tma = tokens && multiple(d_dy, 16) && pitch % 16 == 0 && pitch < (1ull << 40);
+  CUtensorMap map{};
+  if (tma) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return HX_ERR_CUDA;
+    const cuuint64_t dims[2] = {n_out, tokens}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {64, kStep}, unit[2] = {1, 1};
+    if (fn(&map, dtype == HX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+           const_cast<void*>(d_dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return HX_ERR_CUDA;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == HX_F16 ? run<__half>(p, tma, map, a, s) : run<__nv_bfloat16>(p, tma, map, a, s);
+}
+
+}  // extern "C"

@@ -22,6 +22,8 @@ KIND_HUFFMAN, KIND_QLC, KIND_SHANNONIC, KIND_EXPGOLOMB = 0, 1, 2, 3
 CHUNK, SUBSTREAMS, LMAX_MAX, QLC_LMAX = 4096, 8, 12, 11
 CB_SEEN_ONLY = 1
 TABLES_BYTES = 10240
+F32, F16, BF16 = 0, 1, 2
+ROWS_E4M3, ROWS_INT8 = 0, 1
 
 HEADER = os.path.join(_build.INCLUDE, "hx.h")
 
@@ -95,6 +97,17 @@ def lib():
             "hx_session_drain": (i32, [P]),
             "hx_session_batch_info": (i32, [P, u64, ctypes.POINTER(_BatchInfo)]),
             "hx_session_destroy": (None, [P]),
+            "hx_quantize_rows": (i32, [u32, u32, P, u64, u64, u64, P, P, P]),
+            "hx_dequantize_rows": (i32, [u32, u32, P, P, u64, u64, P, u64, P]),
+            "hx_gated_forward": (i32, [u32, u32, P, u64, u64, u64, P, P, P, P]),
+            "hx_gated_backward": (i32, [u32, u32, P, u64, P, P, u64, u64, P, P, P]),
+            "hx_head_norm_rope_forward": (i32, [ctypes.POINTER(_HeadNormRope), P, u64, u64, P, u64, u64,
+                                                P, P, P, P]),
+            "hx_head_norm_rope_workspace": (u64, [u32]),
+            "hx_head_norm_rope_backward": (i32, [ctypes.POINTER(_HeadNormRope), P, u64, u64, P, P, P, u64,
+                                                 u64, P, P, P, u64, P, P]),
+            "hx_weight_grad_workspace": (u64, [u64, u64, u64]),
+            "hx_weight_grad": (i32, [u32, u32, P, u64, P, P, u64, u64, u64, u32, P, u64, i32, P, u64, P, P]),
             "hx_entropy": (ctypes.c_double, [P]),
             "hx_mean_length": (ctypes.c_double, [P, CB]),
             "hx_version": (i32, []),
@@ -114,6 +127,16 @@ def status_string(code: int) -> str:
 def _check(rc: int, what: str) -> None:
     if rc:
         raise HxError(rc, what)
+
+
+class _HeadNormRope(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("weight_dtype", ctypes.c_uint32), ("position_bits", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint64), ("q_heads", ctypes.c_uint32),
+                ("k_heads", ctypes.c_uint32), ("dim", ctypes.c_uint32), ("rot_dim", ctypes.c_uint32),
+                ("interleaved", ctypes.c_uint32), ("eps", ctypes.c_float), ("places", ctypes.c_uint64),
+                ("d_wq", ctypes.c_void_p), ("d_wk", ctypes.c_void_p), ("d_cos", ctypes.c_void_p),
+                ("d_sin", ctypes.c_void_p), ("d_positions", ctypes.c_void_p)]
 
 
 class _SessionConfig(ctypes.Structure):
@@ -483,3 +506,254 @@ class Session:
         h, self._h = getattr(self, "_h", None), None
         if h and _lib is not None:
             _lib.hx_session_destroy(h)
+
+
+# --------------------------------------------------------------------------------- 8-bit rows
+# A matrix kept as bytes (uint8, contiguous) and one float32 scale per row (include/hx.h, "8-bit
+# rows"). Every call runs on the tensors' device and that device's current stream, whichever device is
+# current; outputs are allocated unless they are given.
+def _dtype(t) -> int:
+    import torch
+    d = t.dtype
+    if d is torch.bfloat16:
+        return BF16
+    if d is torch.float32:
+        return F32
+    if d is torch.float16:
+        return F16
+    raise TypeError(f"element type {d} is not float32, float16 or bfloat16")
+
+
+def _on(device):
+    """A context in which `device` is current (None: it already is)."""
+    import torch
+    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _launch(device, what, fn, *args):
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    ctx = _on(device)
+    if ctx is None:
+        rc = fn(*args, stream)
+    else:
+        with ctx:
+            rc = fn(*args, stream)
+    if rc:
+        raise HxError(rc, what)
+
+
+def _cuda(t, what, shape=None, dtype=None, device=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} must have element type {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the other tensors on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _matrix(t, what, shape=None, dtype=None, device=None):
+    """The row stride of a 2-D tensor whose rows are contiguous."""
+    _cuda(t, what, shape, dtype, device)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what} must be a matrix of contiguous rows that do not overlap")
+    return t.stride(0)
+
+
+def _rows8(data, scale, shape, device):
+    """Checks the bytes and scales of 8-bit rows of the given shape (its last entry: the row's length)."""
+    import torch
+    _cuda(data, "bytes", shape, torch.uint8, device)
+    _cuda(scale, "scale", shape[:-1], torch.float32, device)
+    if not data.is_contiguous() or not scale.is_contiguous():
+        raise ValueError("bytes and scale must be contiguous")
+
+
+def _out(t, what, shape, dtype, device):
+    """A contiguous output: the caller's, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _cuda(t, what, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t
+
+
+def _status_ptr(status, device):
+    import torch
+    if status is None:
+        return None
+    _cuda(status, "status", None, torch.int32, device)
+    return status.data_ptr()
+
+
+def quantize_rows(x, fmt: int = ROWS_E4M3, out=None, scale=None):
+    """hx_quantize_rows: the rows of the matrix x as (bytes uint8[rows, cols], scale float32[rows])."""
+    import torch
+    ld = _matrix(x, "x")
+    rows, cols = x.shape
+    out = _out(out, "out", (rows, cols), torch.uint8, x.device)
+    scale = _out(scale, "scale", (rows,), torch.float32, x.device)
+    _launch(x.device, "hx_quantize_rows", lib().hx_quantize_rows, fmt, _dtype(x), x.data_ptr(), rows, cols, ld,
+            out.data_ptr(), scale.data_ptr())
+    return out, scale
+
+
+def dequantize_rows(data, scale, fmt: int = ROWS_E4M3, dtype=None, out=None):
+    """hx_dequantize_rows: the values of 8-bit rows, as `dtype` (default bfloat16) or into the matrix `out`."""
+    import torch
+    _cuda(data, "bytes")
+    if data.dim() != 2:
+        raise ValueError("bytes must be a matrix")
+    _rows8(data, scale, tuple(data.shape), data.device)
+    if out is None:
+        out = torch.empty(data.shape, dtype=dtype or torch.bfloat16, device=data.device)
+    ld = _matrix(out, "out", data.shape, dtype, data.device)
+    _launch(data.device, "hx_dequantize_rows", lib().hx_dequantize_rows, fmt, _dtype(out), data.data_ptr(),
+            scale.data_ptr(), data.shape[0], data.shape[1], out.data_ptr(), ld)
+    return out
+
+
+def gated_forward(x, fmt: int = ROWS_E4M3, save: bool = True, out=None):
+    """hx_gated_forward: silu(gate) * up of x [rows, 2 cols] (gate first). Returns (h, bytes uint8[rows, 2,
+    cols], scale float32[rows, 2]); with save=False (h, None, None)."""
+    import torch
+    ld = _matrix(x, "x")
+    rows, cols = x.shape[0], x.shape[1] // 2
+    if x.shape[1] % 2:
+        raise ValueError("x must have as many gate columns as up columns")
+    out = _out(out, "out", (rows, cols), x.dtype, x.device)
+    data = scale = None
+    if save:
+        data = torch.empty(rows, 2, cols, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(rows, 2, dtype=torch.float32, device=x.device)
+    _launch(x.device, "hx_gated_forward", lib().hx_gated_forward, fmt, _dtype(x), x.data_ptr(), rows, cols, ld,
+            out.data_ptr(), data.data_ptr() if save else None, scale.data_ptr() if save else None)
+    return out, data, scale
+
+
+def gated_backward(dh, data, scale, fmt: int = ROWS_E4M3, need_h: bool = False):
+    """hx_gated_backward: (gradient of x [rows, 2 cols], the activation h again or None) for the gradient dh of
+    gated_forward's output, at the saved gate and up."""
+    import torch
+    ld = _matrix(dh, "dh")
+    rows, cols = dh.shape
+    _rows8(data, scale, (rows, 2, cols), dh.device)
+    dx = torch.empty(rows, 2 * cols, dtype=dh.dtype, device=dh.device)
+    h = torch.empty(rows, cols, dtype=dh.dtype, device=dh.device) if need_h else None
+    _launch(dh.device, "hx_gated_backward", lib().hx_gated_backward, fmt, _dtype(dh), dh.data_ptr(), ld,
+            data.data_ptr(), scale.data_ptr(), rows, cols, dx.data_ptr(), h.data_ptr() if need_h else None)
+    return dx, h
+
+
+def _heads(t, what, shape=None, dtype=None, device=None):
+    """Token and head strides of [tokens, heads, dim] whose heads are contiguous."""
+    _cuda(t, what, shape, dtype, device)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [tokens, heads, dim] with contiguous heads")
+    return t.stride(0), t.stride(1)
+
+
+def _head_norm_rope(t, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt):
+    import torch
+    tokens, heads, dim = t.shape
+    dev = t.device
+    if not 0 <= q_heads <= heads:
+        raise ValueError("q_heads must be between 0 and the number of heads")
+    w = wq if wq is not None else wk
+    if (q_heads and wq is None) or (q_heads < heads and wk is None) or w is None:
+        raise ValueError("a weight is missing")
+    for name, v in (("wq", wq), ("wk", wk)):
+        if v is not None:
+            _cuda(v, name, (dim,), w.dtype, dev)
+            if not v.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    _cuda(cos, "cos", None, torch.float32, dev)
+    _cuda(sin, "sin", cos.shape, torch.float32, dev)
+    if cos.dim() != 2 or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous [places, rot_dim / 2]")
+    _cuda(positions, "positions", (tokens,), None, dev)
+    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous():
+        raise TypeError("positions must be contiguous int64 or int32")
+    return _HeadNormRope(fmt, _dtype(t), _dtype(w), 64 if positions.dtype is torch.int64 else 32, tokens, q_heads,
+                         heads - q_heads, dim, 2 * cos.shape[1], bool(interleaved), eps, cos.shape[0],
+                         wq.data_ptr() if wq is not None else None, wk.data_ptr() if wk is not None else None,
+                         cos.data_ptr(), sin.data_ptr(), positions.data_ptr())
+
+
+def head_norm_rope_forward(x, q_heads: int, wq, wk, cos, sin, positions, eps: float = 1e-6,
+                           interleaved: bool = False, fmt: int = ROWS_E4M3, save: bool = True, out=None,
+                           status=None):
+    """hx_head_norm_rope_forward: norm of each head of x [tokens, heads, dim] (queries, then keys) and the
+    rotation of its first 2 * cos.shape[1] values by row positions[t] of cos and sin. Returns (y, bytes
+    uint8[tokens, heads, dim], scale float32[tokens, heads]); with save=False (y, None, None). `out` may
+    be x."""
+    import torch
+    xt, xh = _heads(x, "x")
+    p = _head_norm_rope(x, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
+    dev = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    yt, yh = _heads(out, "out", x.shape, x.dtype, dev)
+    data = scale = None
+    if save:
+        data = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+        scale = torch.empty(x.shape[:2], dtype=torch.float32, device=dev)
+    _launch(dev, "hx_head_norm_rope_forward", lib().hx_head_norm_rope_forward, ctypes.byref(p), x.data_ptr(), xt, xh,
+            out.data_ptr(), yt, yh, data.data_ptr() if save else None, scale.data_ptr() if save else None,
+            _status_ptr(status, dev))
+    return out, data, scale
+
+
+def head_norm_rope_backward(dy, data, scale, q_heads: int, wq, wk, cos, sin, positions, eps: float = 1e-6,
+                            interleaved: bool = False, fmt: int = ROWS_E4M3, out=None, status=None):
+    """hx_head_norm_rope_backward: (dx, dwq, dwk) at the saved x; the weights' gradients are float32 (None for a
+    weight that is None). `out` (dx) may be dy."""
+    import torch
+    dt, dh = _heads(dy, "dy")
+    p = _head_norm_rope(dy, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
+    dev = dy.device
+    _rows8(data, scale, tuple(dy.shape), dev)
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    ot, oh = _heads(out, "out", dy.shape, dy.dtype, dev)
+    dim = dy.shape[2]
+    ws = torch.empty(lib().hx_head_norm_rope_workspace(dim), dtype=torch.uint8, device=dev)
+    dwq = torch.empty(dim, dtype=torch.float32, device=dev) if wq is not None else None
+    dwk = torch.empty(dim, dtype=torch.float32, device=dev) if wk is not None else None
+    _launch(dev, "hx_head_norm_rope_backward", lib().hx_head_norm_rope_backward, ctypes.byref(p), dy.data_ptr(), dt, dh,
+            data.data_ptr(), scale.data_ptr(), out.data_ptr(), ot, oh, dwq.data_ptr() if dwq is not None else None,
+            dwk.data_ptr() if dwk is not None else None, ws.data_ptr(), ws.numel(), _status_ptr(status, dev))
+    return out, dwq, dwk
+
+
+def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, accumulate: bool = False,
+                status=None):
+    """hx_weight_grad: dY^T X [n_out, n_in] of a linear layer, from dy [tokens, n_out] (float16 or bfloat16) and the
+    8-bit rows of its input X [tokens, n_in]. The result has `dtype` (dy's, or float32), or goes to the
+    matrix `out`, onto its old values if `accumulate`."""
+    import torch
+    ld = _matrix(dy, "dy")
+    tokens, n_out = dy.shape
+    dev = dy.device
+    _cuda(data, "bytes", None, torch.uint8, dev)
+    if data.dim() != 2 or data.shape[0] != tokens:
+        raise ValueError("bytes must be [tokens, n_in]")
+    n_in = data.shape[1]
+    _rows8(data, scale, (tokens, n_in), dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(n_out, n_in, dtype=dtype or dy.dtype, device=dev)
+    ldw = _matrix(out, "out", (n_out, n_in), dtype, dev)
+    need = lib().hx_weight_grad_workspace(tokens, n_out, n_in)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _launch(dev, "hx_weight_grad", lib().hx_weight_grad, fmt, _dtype(dy), dy.data_ptr(), ld, data.data_ptr(),
+            scale.data_ptr(), tokens, n_out, n_in, _dtype(out), out.data_ptr(), ldw, int(accumulate),
+            ws.data_ptr() if need else None, need, _status_ptr(status, dev))
+    return out
