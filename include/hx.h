@@ -421,7 +421,8 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
  * ld_dw) = dY^T X, plus d_dw's old values if accumulate. d_dy: tokens x n_out (row stride ld_dy), dtype
  * HX_F16 or HX_BF16; X: d_bytes (tokens x n_in) and d_scale; dw_dtype: HX_F32 or dtype. The products run
  * on the tensor cores in dtype: X's values are exact there for e4m3 rows in bf16 (and in f16 within its
- * normal range) and rounded once for INT8 rows; sums are in 32 bits. d_workspace:
+ * normal range), and for INT8 rows held as a sum of two (17 bits in bf16, 22 in f16); sums are in 32 bits.
+ * An X beyond f16's range counts as +-65504 with HX_F16. d_workspace:
  * hx_weight_grad_workspace(tokens, n_out, n_in) bytes (0: may be NULL), 16-byte aligned, clobbered.
  * Waits inside the kernel are bounded: HX_ERR_TIMEOUT in *d_status (NULL: not reported). tokens = 0: zeros
  * (or the old values). n_out <= 2^23, n_in <= 2^22. */

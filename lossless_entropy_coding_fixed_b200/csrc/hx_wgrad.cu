@@ -10,8 +10,9 @@
 //   warp 8      brings dY's tile by TMA, in the same swizzle.
 //   warp 9      issues the products.
 // The bytes never exist as a 16-bit matrix in memory. s_t q in bf16 is exact for e4m3 (the scale is a
-// power of two); for INT8 it rounds once, by at most half a step of dY's own type. Sums are the tensor
-// core's 32-bit accumulators.
+// power of two). For INT8 it is not, and one rounding to bf16 would put an error of the size of the result's
+// own rounding into every product: there the tile is held as two, the rounded values and the rounded
+// rest (17 bits together in bf16, 22 in f16), at twice the products. Sums are the tensor core's 32-bit accumulators.
 //
 // Few tiles: the tokens are split over several CTAs per tile, whose 32-bit partial tiles a second
 // kernel adds in order.
@@ -134,13 +135,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-template <int MT, int NT>
+template <int MT, int NT, int kParts>
 struct Tile {
   static constexpr int BM = 128 * MT, BN = NT;
   static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;
-  static constexpr int kStages = 196608 / (kA + kB);
+  static constexpr int kStage = kA + kParts * kB;
+  static constexpr int kStages = 196608 / kStage;
   static constexpr int kCols = MT * NT;  // TMEM columns: a power of two of at least 32
-  static constexpr int kSmem = kStages * (kA + kB) + 1024;
+  static constexpr int kSmem = kStages * kStage + 1024;
   static_assert(kStages >= 2 && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
 };
 
@@ -179,8 +181,8 @@ __device__ __forceinline__ uint4 fetch_dy(const Args& a, uint64_t t, uint32_t c)
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 convert(uint32_t fmt, const Bytes<8>& b, float s) {
+template <typename T, int kParts>
+__device__ __forceinline__ void convert(uint32_t fmt, const Bytes<8>& b, float s, uint4 (&out)[kParts]) {
   float f[8];
   to_values<8>(fmt, b, s, f);
   if constexpr (Type<T>::kInf == 0x7c00u) {
@@ -188,7 +190,19 @@ __device__ __forceinline__ uint4 convert(uint32_t fmt, const Bytes<8>& b, float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = f[i] > 65504.0f ? 65504.0f : f[i] < -65504.0f ? -65504.0f : f[i];
   }
-  return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+      if (p + 1 < kParts) {  // what the rounding left
+        const float2 v = unpack2<T>(r[i]);
+        f[2 * i] -= v.x, f[2 * i + 1] -= v.y;
+      }
+    }
+    out[p] = make_uint4(r[0], r[1], r[2], r[3]);
+  }
 }
 
 __device__ __forceinline__ void put(uint32_t addr, const uint4& v) {
@@ -227,10 +241,10 @@ __device__ __forceinline__ void store_tile(const Args& a, uint32_t row, uint32_t
   }
 }
 
-template <typename T, int MT, int NT, bool kTma>
+template <typename T, int MT, int NT, int kParts, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const Args a) {
-  using S = Tile<MT, NT>;
+  using S = Tile<MT, NT, kParts>;
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bars;
   const uint32_t tiles = (smem_addr(raw) + 1023u) & ~1023u;
@@ -286,13 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
       if (!__all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed))) return false;
-      const uint32_t A = tiles + s * (S::kA + S::kB), B = A + S::kA;
+      const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int tk = token_of(j);
         const float f = __shfl_sync(0xffffffffu, sc[buf], tk);
         const uint32_t ch = NT == 256 ? lane : lane & 15;
-        put(B + (ch >> 3) * 8192 + (warp * 8 + tk) * 128 + (((ch & 7) ^ tk) << 4), convert<T>(a.fmt, b[buf][j], f));
+        uint4 v[kParts];
+        convert<T, kParts>(a.fmt, b[buf][j], f, v);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+          put(B + p * S::kB + (ch >> 3) * 8192 + (warp * 8 + tk) * 128 + (((ch & 7) ^ tk) << 4), v[p]);
       }
       if constexpr (!kTma) {
         const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * 8;
@@ -362,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < S::BM / 64; ++i)
           asm volatile(
               "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                  tiles + s * (S::kA + S::kB) + i * 8192),
+                  tiles + s * S::kStage + i * 8192),
               "l"(&map), "r"((int32_t)(m0 + i * 64)), "r"(t), "r"(copied(s))
               : "memory");
       }
@@ -379,13 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s = k % S::kStages, parity = (k / S::kStages) & 1;
       if (!(ok = bar_wait(converted(s), parity, failed) && (!kTma || bar_wait(copied(s), parity, failed)))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t A = tiles + s * (S::kA + S::kB), B = A + S::kA;
+      const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
 #pragma unroll
       for (int kk = 0; kk < kStep / 16; ++kk)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          mma(tmem + mt * NT, operand(A + mt * 16384 + kk * 2048), operand(B + kk * 2048), instruction<T, NT>(),
-              k > 0 || kk > 0);
+#pragma unroll
+          for (int p = 0; p < kParts; ++p)
+            mma(tmem + mt * NT, operand(A + mt * 16384 + kk * 2048), operand(B + p * S::kB + kk * 2048),
+                instruction<T, NT>(), k > 0 || kk > 0 || p > 0);
       commit(empty(s));
     }
     // the products issued so far end before the TMEM is freed, also when a wait ran out
@@ -443,14 +463,21 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-template <typename T, int MT, int NT, bool kTma>
-int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  using S = Tile<MT, NT>;
-  if (cudaFuncSetAttribute(k_wgrad<T, MT, NT, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+template <typename T, int MT, int NT, int kParts, bool kTma>
+int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  using S = Tile<MT, NT, kParts>;
+  const auto kernel = k_wgrad<T, MT, NT, kParts, kTma>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
     return HX_ERR_CUDA;
   const dim3 grid((a.n_out + S::BM - 1) / S::BM, (a.n_in + S::BN - 1) / S::BN, a.splits);
-  k_wgrad<T, MT, NT, kTma><<<grid, kThreads, S::kSmem, s>>>(map, a);
+  kernel<<<grid, kThreads, S::kSmem, s>>>(map, a);
   return launched();
+}
+template <typename T, int MT, int NT>
+int launch(bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  if (a.fmt == HX_ROWS_E4M3)
+    return tma ? launch_tile<T, MT, NT, 1, true>(map, a, s) : launch_tile<T, MT, NT, 1, false>(map, a, s);
+  return tma ? launch_tile<T, MT, NT, 2, true>(map, a, s) : launch_tile<T, MT, NT, 2, false>(map, a, s);
 }
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
@@ -478,11 +505,7 @@ Plan plan(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
 
 template <typename T>
 int run(const Plan& p, bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  int rc;
-  if (p.big)
-    rc = tma ? launch<T, 2, 256, true>(map, a, s) : launch<T, 2, 256, false>(map, a, s);
-  else
-    rc = tma ? launch<T, 1, 128, true>(map, a, s) : launch<T, 1, 128, false>(map, a, s);
+  const int rc = p.big ? launch<T, 2, 256>(tma, map, a, s) : launch<T, 1, 128>(tma, map, a, s);
   if (rc || a.splits == 1) return rc;
   const uint32_t grid = (uint32_t)std::min<uint64_t>(148 * 8, ceil_div((uint64_t)a.n_out * a.n_in, 256));
   if (a.dw_dtype == HX_F32)

@@ -559,7 +559,8 @@ def _cuda(t, what, shape=None, dtype=None, device=None):
 def _matrix(t, what, shape=None, dtype=None, device=None):
     """The row stride of a 2-D tensor whose rows are contiguous."""
     _cuda(t, what, shape, dtype, device)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    if t.dim() != 2 or (t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1)
+                                       or (t.shape[0] > 1 and t.stride(0) < t.shape[1]))):
         raise ValueError(f"{what} must be a matrix of contiguous rows that do not overlap")
     return t.stride(0)
 
@@ -654,9 +655,22 @@ def gated_backward(dh, data, scale, fmt: int = ROWS_E4M3, need_h: bool = False):
 def _heads(t, what, shape=None, dtype=None, device=None):
     """Token and head strides of [tokens, heads, dim] whose heads are contiguous."""
     _cuda(t, what, shape, dtype, device)
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1 and t.numel()):
         raise ValueError(f"{what} must be [tokens, heads, dim] with contiguous heads")
     return t.stride(0), t.stride(1)
+
+
+def _heads_out(t, shape, dtype, device):
+    """As _heads, for an output: two of its heads may not overlap."""
+    a, b = _heads(t, "out", shape, dtype, device)
+    tokens, heads, dim = shape
+    inner = min((s, n) for s, n in ((a, tokens), (b, heads)) if n > 1) if max(tokens, heads) > 1 else (dim, 1)
+    outer = max(s for s, n in ((a, tokens), (b, heads), (dim, 2)) if n > 1)
+    if not t.numel():
+        return a, b
+    if inner[0] < dim or (min(tokens, heads) > 1 and outer < inner[0] * (inner[1] - 1) + dim):
+        raise ValueError("out must not overlap itself")
+    return a, b
 
 
 def _head_norm_rope(t, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt):
@@ -699,7 +713,7 @@ def head_norm_rope_forward(x, q_heads: int, wq, wk, cos, sin, positions, eps: fl
     dev = x.device
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    yt, yh = _heads(out, "out", x.shape, x.dtype, dev)
+    yt, yh = _heads_out(out, x.shape, x.dtype, dev)
     data = scale = None
     if save:
         data = torch.empty(x.shape, dtype=torch.uint8, device=dev)
@@ -721,7 +735,7 @@ def head_norm_rope_backward(dy, data, scale, q_heads: int, wq, wk, cos, sin, pos
     _rows8(data, scale, tuple(dy.shape), dev)
     if out is None:
         out = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
-    ot, oh = _heads(out, "out", dy.shape, dy.dtype, dev)
+    ot, oh = _heads_out(out, dy.shape, dy.dtype, dev)
     dim = dy.shape[2]
     ws = torch.empty(lib().hx_head_norm_rope_workspace(dim), dtype=torch.uint8, device=dev)
     dwq = torch.empty(dim, dtype=torch.float32, device=dev) if wq is not None else None

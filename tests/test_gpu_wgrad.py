@@ -1,0 +1,197 @@
+"""Weight gradient from 8-bit rows, against the 64-bit product.
+
+Tolerances. The result is rounded once to its type (eps / 2 relative). The products of dY with e4m3 rows in bf16 are
+exact in 32 bits, and each of `tokens` additions loses at most one unit of the last place of 32 bits (2^-23 of the
+sum so far, at most 2^-23 of the sum of the terms' magnitudes); the splits' join adds at most 32 more. INT8 rows are
+held as two values of dY's type: the rest of the rest is within (eps / 2)^2 of each. In f16 a value can fall below the normal
+range: half the smallest subnormal, 2^-25, absolute.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+from lossless_entropy_coding_fixed_b200 import hx  # noqa: E402
+
+from . import _rows as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+FMT = {"e4m3": hx.ROWS_E4M3, "int8": hx.ROWS_INT8}
+
+
+@pytest.fixture(scope="module")
+def cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda:0")
+
+
+def setup(T, n, k, dt, fmt, cuda, seed=0):
+    g = torch.Generator(device=cuda).manual_seed(seed)
+    x = torch.randn(T, k, generator=g, device=cuda) * torch.exp(torch.randn(T, 1, generator=g, device=cuda))
+    if T > 4:
+        x[2] = 0
+    dy = (0.05 * torch.randn(T, n, generator=g, device=cuda)).to(DT[dt])
+    b, s = hx.quantize_rows(x, FMT[fmt])
+    return dy, b, s
+
+
+def check(dw, dy, b, s, dt, fmt, old=None):
+    """All on the GPU in 64 bits: the bytes' values come from a table made on the host."""
+    T = dy.shape[0]
+    table = (ref.values(np.arange(256, dtype=np.uint8)[None], np.ones(1), fmt))[0]
+    table[~np.isfinite(table)] = 0
+    x = torch.from_numpy(table).to(dy.device)[b.long()] * s.double()[:, None]
+    d = dy.double()
+    want, mags = d.T @ x, d.abs().T @ x.abs()
+    if old is not None:
+        want, mags = want + old.double(), mags + old.double().abs()
+    tol = want.abs() * torch.finfo(dw.dtype).eps / 2 + mags * ((T + 64) * 2.0 ** -23)
+    if fmt == "int8":
+        tol = tol + mags * (torch.finfo(DT[dt]).eps / 2) ** 2
+    if dt == "f16":
+        tol = tol + (d.abs().sum(0) * 2.0 ** -25)[:, None]
+    if dw.dtype is torch.float16:
+        tol = tol + 2.0 ** -25
+    assert torch.isfinite(dw).all()
+    assert ((dw.double() - want).abs() <= tol).all()
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (2, 8, 3), (63, 64, 64), (64, 128, 128), (65, 130, 136), (64, 256, 256), (200, 257, 300),
+         (1000, 515, 261), (513, 1024, 512), (5000, 8, 16), (5000, 17, 9), (4096, 64, 64), (20000, 128, 128),
+         (70, 3328, 3200), (129, 3331, 3201), (300, 200, 40000)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("size", SIZES)
+def test_against_the_product(cuda, size, dt, fmt):
+    T, n, k = size
+    dy, b, s = setup(T, n, k, dt, fmt, cuda, seed=T)
+    for out in (dt, "f32"):
+        dw = hx.weight_grad(dy, b, s, FMT[fmt], dtype=DT[out])
+        assert dw.dtype is DT[out] and dw.shape == (n, k)
+        check(dw, dy, b, s, dt, fmt)
+        old = torch.randn(n, k, device=cuda).to(DT[out])
+        dw = hx.weight_grad(dy, b, s, FMT[fmt], out=old.clone(), accumulate=True)
+        check(dw, dy, b, s, dt, fmt, old)
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (8, 0), (8, 8), (1, 0), (16, 4)])
+def test_strides_and_alignment(cuda, T, pad, shift):
+    """dY and dW as parts of wider buffers, bytes on any address; nothing beside dW is written."""
+    n, k = 264, 192
+    dy, b, s = setup(T, n, k, "bf16", "e4m3", cuda, seed=3)
+    want = {o: hx.weight_grad(dy, b, s, dtype=DT[o]) for o in ("bf16", "f32")}
+
+    def inside(rows, cols, dtype, fill):
+        buf = torch.full((rows * (cols + pad) + shift + 16,), fill, dtype=dtype, device=cuda)
+        return buf, buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+    _, v = inside(T, n, torch.bfloat16, float("nan"))  # what lies beside is not read as a value
+    v.copy_(dy)
+    raw = torch.full((T * k + 64,), 0x7f, dtype=torch.uint8, device=cuda)  # NaN's byte
+    at = raw[shift:shift + T * k].view(T, k)
+    at.copy_(b)
+    for o in want:
+        buf, out = inside(n, k, DT[o], 3.0)
+        hx.weight_grad(v, at, s, out=out)
+        assert torch.equal(out, want[o])
+        out.fill_(3.0)
+        assert (buf == 3).all()
+
+
+def test_no_tokens(cuda):
+    dy, b, s = setup(0, 40, 24, "bf16", "e4m3", cuda)
+    assert (hx.weight_grad(dy, b, s) == 0).all()
+    old = torch.randn(40, 24, device=cuda).bfloat16()
+    assert torch.equal(hx.weight_grad(dy, b, s, out=old.clone(), accumulate=True), old)
+
+
+def test_rows_and_columns_of_the_product(cuda):
+    """Each byte's place: one token at a time, one output feature, counted values."""
+    T, n, k = 130, 300, 520
+    x = torch.zeros(T, k, device=cuda)
+    dy = torch.zeros(T, n, device=cuda, dtype=torch.bfloat16)
+    for t in range(T):
+        x[t] = torch.arange(k, device=cuda) % 13 - 6 + t % 3
+        dy[t, (7 * t) % n] = 1 + t % 4
+    b, s = hx.quantize_rows(x, hx.ROWS_E4M3)
+    v = hx.dequantize_rows(b, s, dtype=torch.float32)
+    assert torch.equal(hx.weight_grad(dy, b, s, dtype=torch.float32), (dy.double().T @ v.double()).float())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_a_row_that_was_not_finite(cuda, fmt):
+    dy, b, s = setup(200, 136, 72, "bf16", fmt, cuda)
+    s[77] = float("nan")
+    assert torch.isnan(hx.weight_grad(dy, b, s, FMT[fmt])).all()
+
+
+def test_f16_rows_beyond_its_range(cuda):
+    x = torch.tensor([[65504.0, -65504.0, 1e6, 3.0]], device=cuda)
+    for fmt in (hx.ROWS_E4M3, hx.ROWS_INT8):
+        b, s = hx.quantize_rows(x, fmt)
+        dy = torch.full((1, 8), 0.5, dtype=torch.float16, device=cuda)
+        dw = hx.weight_grad(dy, b, s, fmt, dtype=torch.float32)
+        want = hx.dequantize_rows(b, s, fmt, dtype=torch.float32).clamp(-65504, 65504) * 0.5
+        assert torch.isfinite(dw).all() and torch.allclose(dw, want.expand(8, 4), rtol=2.0 ** -20, atol=0)
+
+
+@pytest.mark.parametrize("size", [(3000, 256, 256), (600, 515, 70), (100, 3328, 3200)])
+def test_repeated_captured_and_two_at_once(cuda, size):
+    """The same bits every time: eager, replayed, and two graphs at once with workspaces of their own."""
+    dy, b, s = setup(*size, "bf16", "int8", cuda)
+    want = hx.weight_grad(dy, b, s, hx.ROWS_INT8)
+    graphs, held = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            held.append(hx.weight_grad(dy, b, s, hx.ROWS_INT8))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(h, want) for h in held) and torch.equal(hx.weight_grad(dy, b, s, hx.ROWS_INT8), want)
+
+
+def test_status_stays_clear(cuda):
+    dy, b, s = setup(300, 200, 100, "bf16", "e4m3", cuda)
+    st = hx.new_status(cuda)
+    hx.weight_grad(dy, b, s, status=st)
+    assert int(st.item()) == 0
+
+
+def test_more_bytes_than_32_bits(cuda):
+    """Tokens and columns whose product passes 2^32."""
+    T, n, k = 1 << 16, 8, (1 << 16) + 64
+    b = torch.zeros(T, k, dtype=torch.uint8, device=cuda)
+    s = torch.ones(T, device=cuda)
+    dy = torch.zeros(T, n, dtype=torch.bfloat16, device=cuda)
+    b[T - 1, k - 5:] = 0x38  # 1.0
+    b[T - 2] = 0x40  # 2.0
+    dy[T - 1, 3], dy[T - 2, 5] = 3, 0.25
+    dw = hx.weight_grad(dy, b, s)
+    want = torch.zeros(n, k, dtype=torch.bfloat16, device=cuda)
+    want[3, k - 5:] = 3
+    want[5] = 0.5
+    assert torch.equal(dw, want)
+
+
+def test_binding_refusals(cuda):
+    dy, b, s = setup(8, 16, 24, "bf16", "e4m3", cuda)
+    for call, err in ((lambda: hx.weight_grad(dy.float(), b, s), hx.HxError),
+                      (lambda: hx.weight_grad(dy, b[:7], s), ValueError),
+                      (lambda: hx.weight_grad(dy, b, s[:7]), ValueError),
+                      (lambda: hx.weight_grad(dy, b.t().contiguous().t(), s), ValueError),
+                      (lambda: hx.weight_grad(dy.t(), b, s), ValueError),
+                      (lambda: hx.weight_grad(dy, b, s, accumulate=True), ValueError),
+                      (lambda: hx.weight_grad(dy, b, s, dtype=torch.float16), hx.HxError),
+                      (lambda: hx.weight_grad(dy, b, s, out=torch.empty(24, 16, device=cuda)), ValueError),
+                      (lambda: hx.weight_grad(dy, b, s, 7), hx.HxError)):
+        with pytest.raises(err):
+            call()
