@@ -50,7 +50,7 @@ struct Args {
 };
 
 // The places of a lane's values: unit j of the lane is vectors of PU values at off0 and off1, whose
-// pairs have the angles `angle` .. angle + PU - 1.
+// pairs have the angles PU u .. PU u + PU - 1 of the token.
 template <int PU, bool kInter>
 struct Units {
   uint32_t units, turned, half;
@@ -64,26 +64,58 @@ struct Units {
   }
 };
 
-// (a, b) -> (a c - b s, b c + a s), pairs across the two vectors or (kInter) inside them.
+// A lane's 16 values as 8 slots of two, for the packed 32-bit arithmetic. Vectors of 2 or more: slots
+// are neighbours, first those of vector 0, then those of vector 1; vectors of 1: slot j is unit j's (a, b).
+// The other value of a pair is in the same slot (kSwap) or in the same place of the other vector.
 template <int PU, bool kInter>
-__device__ __forceinline__ void turn(float (&a)[PU], float (&b)[PU], const float (&c)[PU],
-                                     const float (&s)[PU]) {
-  if constexpr (!kInter) {
-#pragma unroll
-    for (int i = 0; i < PU; ++i) {
-      const float v = a[i] * c[i] - b[i] * s[i];
-      b[i] = b[i] * c[i] + a[i] * s[i];
-      a[i] = v;
-    }
+struct Slots {
+  static constexpr int N = 8 / PU, H = PU / 2;
+  static constexpr bool kSwap = kInter || PU == 1;
+  // the slot that holds the pairs' other values, to be swapped if kSwap
+  static constexpr __device__ int other(int k) { return kSwap ? k : k % PU < H ? k + H : k - H; }
+  static constexpr __device__ bool second(int k) { return !kSwap && k % PU >= H; }
+};
+
+__device__ __forceinline__ uint64_t as_u64(float2 v) {
+  return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 as_f2(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
+
+template <int PU>
+__device__ __forceinline__ void to_slots(int j, const float (&f0)[PU], const float (&f1)[PU], float2 (&v)[8]) {
+  if constexpr (PU == 1) {
+    v[j] = make_float2(f0[0], f1[0]);
   } else {
-    // pair i is values 2i, 2i + 1 of the two vectors one after the other
 #pragma unroll
-    for (int i = 0; i < PU; ++i) {
-      float& p = 2 * i < PU ? a[(2 * i) % PU] : b[(2 * i) % PU];
-      float& q = 2 * i + 1 < PU ? a[(2 * i + 1) % PU] : b[(2 * i + 1) % PU];
-      const float v = p * c[i] - q * s[i];
-      q = q * c[i] + p * s[i];
-      p = v;
+    for (int i = 0; i < PU / 2; ++i) {
+      v[j * PU + i] = make_float2(f0[2 * i], f0[2 * i + 1]);
+      v[j * PU + PU / 2 + i] = make_float2(f1[2 * i], f1[2 * i + 1]);
+    }
+  }
+}
+template <int PU>
+__device__ __forceinline__ void from_slots(int j, const float2 (&v)[8], float (&f0)[PU], float (&f1)[PU]) {
+  if constexpr (PU == 1) {
+    f0[0] = v[j].x, f1[0] = v[j].y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PU / 2; ++i) {
+      f0[2 * i] = v[j * PU + i].x, f0[2 * i + 1] = v[j * PU + i].y;
+      f1[2 * i] = v[j * PU + PU / 2 + i].x, f1[2 * i + 1] = v[j * PU + PU / 2 + i].y;
     }
   }
 }
@@ -98,148 +130,189 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t lanes) {
 }
 
 template <typename T, int PU, bool kInter>
-__device__ __forceinline__ void load_weight(const Args& a, const void* w, uint32_t sub,
-                                            float (&w0)[8 / PU][PU], float (&w1)[8 / PU][PU]) {
+__device__ __forceinline__ void load_weight(const Args& a, const void* w, uint32_t sub, float2 (&out)[8]) {
   const Units<PU, kInter> un(a);
 #pragma unroll
   for (int j = 0; j < 8 / PU; ++j) {
     const uint32_t u = j * a.lanes + sub;
+    float f0[PU], f1[PU];
     if (!un.has(u)) {
 #pragma unroll
-      for (int i = 0; i < PU; ++i) w0[j][i] = w1[j][i] = 0.0f;
+      for (int i = 0; i < PU; ++i) f0[i] = f1[i] = 0.0f;
     } else if (a.w_f32) {
       Vec<float, PU> v;
       v.load(static_cast<const float*>(w) + un.off0(u));
-      v.floats(w0[j]);
+      v.floats(f0);
       v.load(static_cast<const float*>(w) + un.off1(u));
-      v.floats(w1[j]);
+      v.floats(f1);
     } else {
       Vec<T, PU> v;
       v.load(static_cast<const T*>(w) + un.off0(u));
-      v.floats(w0[j]);
+      v.floats(f0);
       v.load(static_cast<const T*>(w) + un.off1(u));
-      v.floats(w1[j]);
+      v.floats(f1);
     }
+    to_slots<PU>(j, f0, f1, out);
   }
 }
 
-// The token's cosines and sines of the lane's pairs (1 and 0 for values that are not turned).
-// Returns false, and leaves (1, 0), for a position outside the tables.
+// The token's turn of the lane's slots: v -> v * c + (the pairs' other values) * s; c = 1 and s = 0
+// where nothing turns. `sign` 1: forward; -1: back. Returns false, with nothing turned, for a
+// position outside the tables.
 template <int PU, bool kInter>
-__device__ __forceinline__ bool load_angles(const Args& a, uint64_t t, uint32_t sub, float sign,
-                                            float (&c)[8 / PU][PU], float (&s)[8 / PU][PU]) {
+__device__ __forceinline__ bool load_turn(const Args& a, uint64_t t, uint32_t sub, float sign, float2 (&c)[8],
+                                          float2 (&s)[8]) {
+  using S = Slots<PU, kInter>;
   const Units<PU, kInter> un(a);
   const int64_t p = a.pos64 ? static_cast<const int64_t*>(a.pos)[t]
                             : (int64_t) static_cast<const int32_t*>(a.pos)[t];
   const bool ok = p >= 0 && (uint64_t)p < a.places;
 #pragma unroll
-  for (int j = 0; j < 8 / PU; ++j) {
+  for (int j = 0; j < S::N; ++j) {
     const uint32_t u = j * a.lanes + sub;
+    float fc[PU], fs[PU];
+#pragma unroll
+    for (int i = 0; i < PU; ++i) fc[i] = 1.0f, fs[i] = 0.0f;
     if (ok && un.turns(u)) {
       const uint64_t at = (uint64_t)p * un.half + PU * u;
       Vec<float, PU> v;
       v.load(a.cos + at);
-      v.floats(c[j]);
+      v.floats(fc);
       v.load(a.sin + at);
-      v.floats(s[j]);
+      v.floats(fs);
+    }
+    // pair (a, b) -> (a c - b s, b c + a s)
 #pragma unroll
-      for (int i = 0; i < PU; ++i) s[j][i] *= sign;
-    } else {
-#pragma unroll
-      for (int i = 0; i < PU; ++i) c[j][i] = 1.0f, s[j][i] = 0.0f;
+    for (int i = 0; i < PU; ++i) {
+      if constexpr (S::kSwap) {
+        c[j * PU + i] = both(fc[i]);
+        s[j * PU + i] = make_float2(-sign * fs[i], sign * fs[i]);
+      } else if (i < S::H) {
+        c[j * PU + i] = c[j * PU + S::H + i] = make_float2(fc[(2 * i) % PU], fc[(2 * i + 1) % PU]);
+        const float2 v = make_float2(sign * fs[(2 * i) % PU], sign * fs[(2 * i + 1) % PU]);
+        s[j * PU + i] = make_float2(-v.x, -v.y);
+        s[j * PU + S::H + i] = v;
+      }
     }
   }
   if (!ok && a.status && sub == 0) atomicOr(a.status, (uint32_t)HX_ERR_ARG);
   return ok;
 }
 
+// Item i as (token, chunk of heads).
+__device__ __forceinline__ void split_item(uint64_t i, uint32_t chunks, uint64_t& t, uint32_t& ch) {
+  t = i >> 32 ? i / chunks : (uint32_t)i / chunks;
+  ch = (uint32_t)(i - t * chunks);
+}
+
+// With the weight folded into the turn, y = r (x * (w c) + other(x) * (other(w) s)): the products
+// w c and w s are made once per token and group of heads.
 template <typename T, int PU, bool kInter>
-__global__ void __launch_bounds__(kThreads) k_qk_forward(const Args a) {
-  constexpr int N = 8 / PU;
+__global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constant__ Args a) {
+  using S = Slots<PU, kInter>;
   const Units<PU, kInter> un(a);
   const uint32_t sub = threadIdx.x % a.lanes, groups = kThreads / a.lanes;
   const uint64_t item = blockIdx.x * (uint64_t)groups + threadIdx.x / a.lanes;
   const uint32_t cq = (a.nq + a.per - 1) / a.per, chunks = cq + (a.nk + a.per - 1) / a.per;
   const bool live = item < a.tokens * chunks;
-  const uint64_t t = live ? item / chunks : 0;
-  const uint32_t ch = live ? (uint32_t)(item - t * chunks) : 0;
+  uint64_t t = 0;
+  uint32_t ch = 0;
+  if (live) split_item(item, chunks, t, ch);
   const bool key = ch >= cq;
   const uint32_t h0 = key ? a.nq + (ch - cq) * a.per : ch * a.per;
   const uint32_t h1 = live ? min(h0 + a.per, key ? a.nq + a.nk : a.nq) : h0;
 
-  float w0[N][PU], w1[N][PU], c[N][PU], s[N][PU];
-  Vec<T, PU> v0[N], v1[N];
-  const T* x = static_cast<const T*>(a.x) + t * a.xt;
-  T* y = static_cast<T*>(a.y) + t * a.yt;
-  auto fetch = [&](uint32_t h) {
+  Vec<T, PU> v0[S::N], v1[S::N];
+  const T* x = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
+  T* y = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
+  uint64_t row = t * (a.nq + a.nk) + h0;
+  auto fetch = [&](bool any) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < S::N; ++j) {
       const uint32_t u = j * a.lanes + sub;
-      if (h < h1 && un.has(u)) {
-        v0[j].load(x + h * a.xh + un.off0(u));
-        v1[j].load(x + h * a.xh + un.off1(u));
+      if (any && un.has(u)) {
+        v0[j].load(x + un.off0(u));
+        v1[j].load(x + un.off1(u));
       } else {
         v0[j].zero();
         v1[j].zero();
       }
     }
+    x += a.xh;
   };
-  fetch(h0);
-  load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w0, w1);
-  const bool ok = load_angles<PU, kInter>(a, t, sub, 1.0f, c, s);
+  fetch(h0 < h1);
+  float2 c[8], s[8];
+  bool ok;
+  {
+    float2 w[8];
+    load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w);
+    ok = load_turn<PU, kInter>(a, t, sub, 1.0f, c, s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c[k] = mul2(c[k], w[k]);
+      s[k] = mul2(s[k], S::kSwap ? swapped(w[k]) : w[S::other(k)]);
+    }
+  }
+  const float part = 1.0f / (float)a.dim;
   for (uint32_t k = 0; k < a.per; ++k) {  // the same count in every lane: the butterflies need all
     const uint32_t h = h0 + k;
-    float f0[N][PU], f1[N][PU];
-    float sq = 0.0f;
+    float2 v[8], q = both(0.0f);
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v0[j].floats(f0[j]);
-      v1[j].floats(f1[j]);
-      top = v1[j].top(v0[j].top(top));
-#pragma unroll
-      for (int i = 0; i < PU; ++i) sq += f0[j][i] * f0[j][i] + f1[j][i] * f1[j][i];
+    for (int j = 0; j < S::N; ++j) {
+      float f0[PU], f1[PU];
+      v0[j].floats(f0);
+      v1[j].floats(f1);
+      to_slots<PU>(j, f0, f1, v);
+      if (a.bytes) top = v1[j].top(v0[j].top(top));
     }
-    fetch(h + 1);
-    sq = group_sum(sq, a.lanes);
-    float r = 1.0f / sqrtf(sq / (float)a.dim + a.eps);
+    fetch(h + 1 < h1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q = fma2(v[i], v[i], q);
+    const float sq = group_sum(q.x + q.y, a.lanes);
+    float r = rsqrtf(fmaf(sq, part, a.eps));
     if (!ok) r = __uint_as_float(0x7fc00000u);
     if (a.bytes) {
       top = group_max(top_bits<T>(top), a.lanes);
       const Scale sc = scale_of<T>(a.fmt, top);
       if (h < h1) {
-        const uint64_t row = t * (a.nq + a.nk) + h;
         if (sub == 0) a.scale[row] = sc.s;
+        uint8_t* b = a.bytes + row * a.dim;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < S::N; ++j) {
           const uint32_t u = j * a.lanes + sub;
           if (!un.has(u)) continue;
-          to_bytes<PU>(a.fmt, f0[j], sc).store(a.bytes + row * a.dim + un.off0(u));
-          to_bytes<PU>(a.fmt, f1[j], sc).store(a.bytes + row * a.dim + un.off1(u));
+          float f0[PU], f1[PU];
+          from_slots<PU>(j, v, f0, f1);
+          to_bytes<PU>(a.fmt, f0, sc).store(b + un.off0(u));
+          to_bytes<PU>(a.fmt, f1, sc).store(b + un.off1(u));
         }
       }
     }
+    float2 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = mul2(fma2(v[i], c[i], mul2(S::kSwap ? swapped(v[i]) : v[S::other(i)], s[i])), both(r));
     if (h < h1) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
+      for (int j = 0; j < S::N; ++j) {
         const uint32_t u = j * a.lanes + sub;
         if (!un.has(u)) continue;
-#pragma unroll
-        for (int i = 0; i < PU; ++i) {
-          f0[j][i] = f0[j][i] * r * w0[j][i];
-          f1[j][i] = f1[j][i] * r * w1[j][i];
-        }
-        if (un.turns(u)) turn<PU, kInter>(f0[j], f1[j], c[j], s[j]);
-        store<T, PU>(y + h * a.yh + un.off0(u), f0[j]);
-        store<T, PU>(y + h * a.yh + un.off1(u), f1[j]);
+        float f0[PU], f1[PU];
+        from_slots<PU>(j, o, f0, f1);
+        store<T, PU>(y + un.off0(u), f0);
+        store<T, PU>(y + un.off1(u), f1);
       }
     }
+    y += a.yh;
+    ++row;
   }
 }
 
+// In terms of the bytes' values q (x~ = s q): n = q s r, dw += g n, dx = r (g w - n mean(g w n)).
 template <typename T, int PU, bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const Args a) {
-  constexpr int N = 8 / PU;
+__global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_constant__ Args a) {
+  using S = Slots<PU, kInter>;
   __shared__ float sums[kThreads * 16];
   const Units<PU, kInter> un(a);
   const uint32_t sub = threadIdx.x % a.lanes, groups = kThreads / a.lanes;
@@ -250,37 +323,39 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const Args a) {
   const uint32_t blocks = key ? gridDim.x - a.blocks_q : a.blocks_q;
   const uint32_t block = key ? blockIdx.x - a.blocks_q : blockIdx.x;
   const uint64_t items = a.tokens * chunks;
+  const float part = 1.0f / (float)a.dim;
 
-  float w0[N][PU], w1[N][PU], d0[N][PU], d1[N][PU];
-  load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w0, w1);
+  float2 w[8], dw[8];
+  load_weight<T, PU, kInter>(a, key ? a.wk : a.wq, sub, w);
 #pragma unroll
-  for (int j = 0; j < N; ++j)
-#pragma unroll
-    for (int i = 0; i < PU; ++i) d0[j][i] = d1[j][i] = 0.0f;
+  for (int i = 0; i < 8; ++i) dw[i] = both(0.0f);
 
   for (uint64_t base = (uint64_t)block * groups; base < items; base += (uint64_t)blocks * groups) {
     const uint64_t item = base + group;
     const bool live = item < items;
-    const uint64_t t = live ? item / chunks : 0;
-    const uint32_t h0 = first + (live ? (uint32_t)(item - t * chunks) : 0) * a.per;
+    uint64_t t = 0;
+    uint32_t ch = 0;
+    if (live) split_item(item, chunks, t, ch);
+    const uint32_t h0 = first + ch * a.per;
     const uint32_t h1 = live ? min(h0 + a.per, first + heads) : h0;
-    float c[N][PU], s[N][PU];
-    Vec<T, PU> v0[N], v1[N];
-    Bytes<PU> b0[N], b1[N];
+    float2 c[8], s[8];
+    Vec<T, PU> v0[S::N], v1[S::N];
+    Bytes<PU> b0[S::N], b1[S::N];
     float sc = 0.0f;
-    const T* dy = static_cast<const T*>(a.x) + t * a.xt;
-    T* dx = static_cast<T*>(a.y) + t * a.yt;
-    auto fetch = [&](uint32_t h) {
-      const uint64_t row = t * (a.nq + a.nk) + h;
-      sc = h < h1 ? a.scale[row] : 0.0f;
+    const T* dy = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
+    T* dx = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
+    uint64_t row = t * (a.nq + a.nk) + h0;
+    const uint8_t* bytes = a.bytes + row * a.dim;
+    auto fetch = [&](bool any) {
+      sc = any ? a.scale[row] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
+      for (int j = 0; j < S::N; ++j) {
         const uint32_t u = j * a.lanes + sub;
-        if (h < h1 && un.has(u)) {
-          v0[j].load(dy + h * a.xh + un.off0(u));
-          v1[j].load(dy + h * a.xh + un.off1(u));
-          b0[j].load(a.bytes + row * a.dim + un.off0(u));
-          b1[j].load(a.bytes + row * a.dim + un.off1(u));
+        if (any && un.has(u)) {
+          v0[j].load(dy + un.off0(u));
+          v1[j].load(dy + un.off1(u));
+          b0[j].load(bytes + un.off0(u));
+          b1[j].load(bytes + un.off1(u));
         } else {
           v0[j].zero();
           v1[j].zero();
@@ -288,67 +363,80 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const Args a) {
           for (int i = 0; i < Bytes<PU>::kRaw; ++i) b0[j].b[i] = b1[j].b[i] = 0;
         }
       }
+      dy += a.xh;
+      bytes += a.dim;
+      ++row;
     };
-    fetch(h0);
-    bool ok = true;
-    if (live) ok = load_angles<PU, kInter>(a, t, sub, -1.0f, c, s);
+    fetch(h0 < h1);
+    // (token 0's for an item that is not live: its heads are empty)
+    const bool ok = load_turn<PU, kInter>(a, t, sub, -1.0f, c, s);
     for (uint32_t k = 0; k < a.per; ++k) {
       const uint32_t h = h0 + k;
-      float g0[N][PU], g1[N][PU], x0[N][PU], x1[N][PU];
-      float sq = 0.0f, dot = 0.0f;
+      float2 g[8], q[8];
+      const float scale = sc;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        v0[j].floats(g0[j]);
-        v1[j].floats(g1[j]);
-        to_values<PU>(a.fmt, b0[j], sc, x0[j]);
-        to_values<PU>(a.fmt, b1[j], sc, x1[j]);
+      for (int j = 0; j < S::N; ++j) {
+        float f0[PU], f1[PU];
+        v0[j].floats(f0);
+        v1[j].floats(f1);
+        to_slots<PU>(j, f0, f1, g);
+        to_values<PU>(a.fmt, b0[j], 1.0f, f0);
+        to_values<PU>(a.fmt, b1[j], 1.0f, f1);
+        to_slots<PU>(j, f0, f1, q);
       }
-      fetch(h + 1);
+      fetch(h + 1 < h1);
+      {
+        float2 o[8];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint32_t u = j * a.lanes + sub;
-        if (h < h1 && un.turns(u)) turn<PU, kInter>(g0[j], g1[j], c[j], s[j]);
+        for (int i = 0; i < 8; ++i) o[i] = fma2(g[i], c[i], mul2(S::kSwap ? swapped(g[i]) : g[S::other(i)], s[i]));
 #pragma unroll
-        for (int i = 0; i < PU; ++i) {
-          sq += x0[j][i] * x0[j][i] + x1[j][i] * x1[j][i];
-          dot += g0[j][i] * w0[j][i] * x0[j][i] + g1[j][i] * w1[j][i] * x1[j][i];
-        }
+        for (int i = 0; i < 8; ++i) g[i] = o[i];
       }
-      sq = group_sum(sq, a.lanes);
-      dot = group_sum(dot, a.lanes);
-      float r = 1.0f / sqrtf(sq / (float)a.dim + a.eps);
+      float2 sq2 = both(0.0f), dot2 = both(0.0f), gq[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sq2 = fma2(q[i], q[i], sq2);
+        gq[i] = mul2(g[i], q[i]);
+        dot2 = fma2(gq[i], w[i], dot2);
+      }
+      const float sq = group_sum(sq2.x + sq2.y, a.lanes) * scale * scale;
+      const float dot = group_sum(dot2.x + dot2.y, a.lanes) * scale;
+      float r = rsqrtf(fmaf(sq, part, a.eps));
       if (!ok) r = __uint_as_float(0x7fc00000u);
-      const float m = dot * r / (float)a.dim;  // mean(d x~ r)
+      const float sr = scale * r;                // n = q sr
+      const float2 m = both(-dot * r * part * sr * r);  // dx = g w r - q (mean(g w n) s r r)
       if (h < h1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int i = 0; i < 8; ++i) {
+          dw[i] = fma2(gq[i], both(sr), dw[i]);
+          g[i] = fma2(mul2(g[i], w[i]), both(r), mul2(q[i], m));
+        }
+#pragma unroll
+        for (int j = 0; j < S::N; ++j) {
           const uint32_t u = j * a.lanes + sub;
           if (!un.has(u)) continue;
-#pragma unroll
-          for (int i = 0; i < PU; ++i) {
-            const float n0 = x0[j][i] * r, n1 = x1[j][i] * r;
-            d0[j][i] += g0[j][i] * n0;
-            d1[j][i] += g1[j][i] * n1;
-            g0[j][i] = r * (g0[j][i] * w0[j][i] - n0 * m);
-            g1[j][i] = r * (g1[j][i] * w1[j][i] - n1 * m);
-          }
-          store<T, PU>(dx + h * a.yh + un.off0(u), g0[j]);
-          store<T, PU>(dx + h * a.yh + un.off1(u), g1[j]);
+          float f0[PU], f1[PU];
+          from_slots<PU>(j, g, f0, f1);
+          store<T, PU>(dx + un.off0(u), f0);
+          store<T, PU>(dx + un.off1(u), f1);
         }
       }
+      dx += a.yh;
     }
   }
 
   // the block's sum of its groups' weight gradients, in the groups' order
   float* mine = sums + group * (16 * a.lanes);
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
+  for (int j = 0; j < S::N; ++j) {
     const uint32_t u = j * a.lanes + sub;
     if (!un.has(u)) continue;
+    float f0[PU], f1[PU];
+    from_slots<PU>(j, dw, f0, f1);
 #pragma unroll
     for (int i = 0; i < PU; ++i) {
-      mine[un.off0(u) + i] = d0[j][i];
-      mine[un.off1(u) + i] = d1[j][i];
+      mine[un.off0(u) + i] = f0[i];
+      mine[un.off1(u) + i] = f1[i];
     }
   }
   __syncthreads();

@@ -4,11 +4,11 @@
 // A product of two matrices whose contraction runs over the tokens, so both operands are stored with
 // the contraction outermost (MN-major). Tensor cores: tcgen05.mma, accumulators in TMEM, one CTA
 // per tile of BM output by BN input features, steps of 64 tokens.
-//   warps 0-7   read the bytes (8 columns of a token per lane, the next steps' already in flight),
+//   warps 0-15  read the bytes (8 columns of a token per lane, the next steps' already in flight),
 //               turn them into s_t q in dY's type and write them to shared memory in the 128-byte
 //               swizzle that the tensor core reads; at the end they read TMEM and store the tile.
-//   warp 8      brings dY's tile by TMA, in the same swizzle.
-//   warp 9      issues the products.
+//   warp 16     brings dY's tile by TMA, in the same swizzle.
+//   warp 17     issues the products.
 // The bytes never exist as a 16-bit matrix in memory. s_t q in bf16 is exact for e4m3 (the scale is a
 // power of two). For INT8 it is not, and one rounding to bf16 would put an error of the size of the result's
 // own rounding into every product: there the tile is held as two, the rounded values and the rounded
@@ -33,8 +33,9 @@ namespace {
 using namespace hxv;
 
 constexpr int kStep = 64;             // tokens per pipeline stage
-constexpr int kConvert = 256;         // converting threads (warps 0-7)
-constexpr int kThreads = kConvert + 64;
+constexpr int kWarps = 16;            // converting warps
+constexpr int kTokens = kStep / kWarps;  // a converting warp's tokens of a stage
+constexpr int kThreads = 32 * (kWarps + 2);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxSplits = 32;
 
@@ -261,14 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       bar_init(copied(s), 1);
-      bar_init(converted(s), kConvert / 32);
+      bar_init(converted(s), kWarps);
       bar_init(empty(s), 1);
     }
     bar_init(done, 1);
     bars.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
                  "r"((uint32_t)S::kCols)
                  : "memory");
@@ -279,22 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
 
-  if (warp < 8) {
-    // ---- converting warps: tokens 8 warp .. 8 warp + 7 of every step
+  if (warp < kWarps) {
+    // ---- converting warps: tokens kTokens * warp .. of every step
     // 8 columns per lane: a warp's load is one token's 256 columns, or two tokens' 128 (lanes
     // 16-31 the odd one). Lanes 8 i .. 8 i + 7 write one whole line, so no two share a bank.
     static_assert(NT == 256 || NT == 128, "");
-    constexpr int kLoads = NT == 256 ? 8 : 4;
+    constexpr int kLoads = NT == 256 ? kTokens : kTokens / 2;
     Bytes<8> b[2][kLoads];
     float sc[2];
     auto token_of = [&](int j) { return NT == 256 ? j : 2 * j + (int)(lane >> 4); };
     auto fetch = [&](uint32_t k, int buf) {
-      const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * 8;
+      const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * kTokens;
       const uint32_t c = n0 + (NT == 256 ? lane : lane & 15) * 8;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) b[buf][j] = fetch_bytes(a, k < steps ? t + token_of(j) : a.tokens, c);
       sc[buf] = 0.0f;
-      if (k < steps && t + (lane & 7) < a.tokens) sc[buf] = a.scale[t + (lane & 7)];
+      if (k < steps && t + (lane & (kTokens - 1)) < a.tokens) sc[buf] = a.scale[t + (lane & (kTokens - 1))];
     };
     auto one = [&](uint32_t k, int buf) {
       const uint32_t s = k % S::kStages;
@@ -305,20 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kLoads; ++j) {
         const int tk = token_of(j);
         const float f = __shfl_sync(0xffffffffu, sc[buf], tk);
-        const uint32_t ch = NT == 256 ? lane : lane & 15;
+        const uint32_t ch = NT == 256 ? lane : lane & 15, line = warp * kTokens + tk;
         uint4 v[kParts];
         convert<T, kParts>(a.fmt, b[buf][j], f, v);
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
-          put(B + p * S::kB + (ch >> 3) * 8192 + (warp * 8 + tk) * 128 + (((ch & 7) ^ tk) << 4), v[p]);
+          put(B + p * S::kB + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), v[p]);
       }
       if constexpr (!kTma) {
-        const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * 8;
+        const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * kTokens;
         for (int h = 0; h < S::BM; h += 256)
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t ch = h / 8 + lane;
+          for (int j = 0; j < kTokens; ++j) {
+            const uint32_t ch = h / 8 + lane, line = warp * kTokens + j;
             if (ch * 8 < S::BM)
-              put(A + (ch >> 3) * 8192 + (warp * 8 + j) * 128 + (((ch & 7) ^ j) << 4), fetch_dy<T>(a, t + j, m0 + ch * 8));
+              put(A + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), fetch_dy<T>(a, t + j, m0 + ch * 8));
           }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -340,8 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && steps) ok = bar_wait(done, 0, failed);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (__all_sync(0xffffffffu, ok)) {
-      const uint32_t mt = MT == 2 ? warp >> 2 : 0;
-      const uint32_t c0 = MT == 2 ? 0 : (warp >> 2) * (NT / 2), c1 = MT == 2 ? NT : c0 + NT / 2;
+      const uint32_t mt = (warp >> 2) % MT;
+      constexpr uint32_t kWidth = NT * 4 * MT / kWarps;  // columns per warp
+      const uint32_t c0 = (warp >> 2) / MT * kWidth, c1 = c0 + kWidth;
       const uint32_t row = m0 + mt * 128 + (warp & 3) * 32 + lane;
       for (uint32_t c = c0; c < c1; c += 32) {
         uint32_t r[32];
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  } else if (warp == 8) {
+  } else if (warp == kWarps) {
     if (kTma && lane == 0) {
       uint32_t k = 0;
       for (; k < steps; ++k) {
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   __syncthreads();
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kCols));

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -101,10 +102,10 @@ def lib():
             "hx_dequantize_rows": (i32, [u32, u32, P, P, u64, u64, P, u64, P]),
             "hx_gated_forward": (i32, [u32, u32, P, u64, u64, u64, P, P, P, P]),
             "hx_gated_backward": (i32, [u32, u32, P, u64, P, P, u64, u64, P, P, P]),
-            "hx_head_norm_rope_forward": (i32, [ctypes.POINTER(_HeadNormRope), P, u64, u64, P, u64, u64,
+            "hx_head_norm_rope_forward": (i32, [P, P, u64, u64, P, u64, u64,
                                                 P, P, P, P]),
             "hx_head_norm_rope_workspace": (u64, [u32]),
-            "hx_head_norm_rope_backward": (i32, [ctypes.POINTER(_HeadNormRope), P, u64, u64, P, P, P, u64,
+            "hx_head_norm_rope_backward": (i32, [P, P, u64, u64, P, P, P, u64,
                                                  u64, P, P, P, u64, P, P]),
             "hx_weight_grad_workspace": (u64, [u64, u64, u64]),
             "hx_weight_grad": (i32, [u32, u32, P, u64, P, P, u64, u64, u64, u32, P, u64, i32, P, u64, P, P]),
@@ -511,193 +512,211 @@ class Session:
 # --------------------------------------------------------------------------------- 8-bit rows
 # A matrix kept as bytes (uint8, contiguous) and one float32 scale per row (include/hx.h, "8-bit
 # rows"). Every call runs on the tensors' device and that device's current stream, whichever device is
-# current; outputs are allocated unless they are given.
+# current; outputs are allocated unless they are given. A small call's time is its host time, so the
+# checks are plain comparisons and the stream is read as the raw handle.
+_torch = None
+
+
+def _load_torch():
+    global _torch, _DTYPES, _raw_stream, _current_device
+    import torch
+    _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
+    return torch
+
+
 def _dtype(t) -> int:
-    import torch
-    d = t.dtype
-    if d is torch.bfloat16:
-        return BF16
-    if d is torch.float32:
-        return F32
-    if d is torch.float16:
-        return F16
-    raise TypeError(f"element type {d} is not float32, float16 or bfloat16")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"element type {t.dtype} is not float32, float16 or bfloat16")
+    return d
 
 
-def _on(device):
-    """A context in which `device` is current (None: it already is)."""
-    import torch
-    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _launch(device, what, fn, *args):
-    import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
-    ctx = _on(device)
-    if ctx is None:
-        rc = fn(*args, stream)
+def _launch(dev, what, fn, *args):
+    """fn(*args, the current stream of device `dev`), with that device current."""
+    if _current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with ctx:
-            rc = fn(*args, stream)
+        with _torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     if rc:
         raise HxError(rc, what)
 
 
-def _cuda(t, what, shape=None, dtype=None, device=None):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _device(t, what) -> int:
+    """The index of the CUDA device of the tensor t."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{what} must have element type {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the other tensors on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    return t.get_device()
+
+
+def _same(t, what, shape, dtype, dev):
+    """Checks a tensor's device, element type and shape."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must have element type {dtype}, not {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on another device than the other tensors")
 
 
-def _matrix(t, what, shape=None, dtype=None, device=None):
-    """The row stride of a 2-D tensor whose rows are contiguous."""
-    _cuda(t, what, shape, dtype, device)
-    if t.dim() != 2 or (t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1)
-                                       or (t.shape[0] > 1 and t.stride(0) < t.shape[1]))):
-        raise ValueError(f"{what} must be a matrix of contiguous rows that do not overlap")
-    return t.stride(0)
-
-
-def _rows8(data, scale, shape, device):
-    """Checks the bytes and scales of 8-bit rows of the given shape (its last entry: the row's length)."""
-    import torch
-    _cuda(data, "bytes", shape, torch.uint8, device)
-    _cuda(scale, "scale", shape[:-1], torch.float32, device)
-    if not data.is_contiguous() or not scale.is_contiguous():
-        raise ValueError("bytes and scale must be contiguous")
-
-
-def _out(t, what, shape, dtype, device):
-    """A contiguous output: the caller's, checked, or a new one."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _cuda(t, what, shape, dtype, device)
+def _dense(t, what, shape, dtype, dev) -> int:
+    """Checks a contiguous tensor; its address."""
+    _same(t, what, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _status_ptr(status, device):
-    import torch
+def _matrix(t, what):
+    """(rows, cols, row stride) of a matrix whose rows are contiguous and do not overlap."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be a matrix")
+    rows, cols = shape
+    if (stride[1] != 1 and cols > 1 or stride[0] < cols and rows > 1) and rows and cols:
+        raise ValueError(f"{what} must be a matrix of contiguous rows that do not overlap")
+    return rows, cols, stride[0]
+
+
+def _status_ptr(status, dev):
     if status is None:
         return None
-    _cuda(status, "status", None, torch.int32, device)
+    if _device(status, "status") != dev or status.dtype is not _torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 status word on the tensors' device")
     return status.data_ptr()
 
 
 def quantize_rows(x, fmt: int = ROWS_E4M3, out=None, scale=None):
     """hx_quantize_rows: the rows of the matrix x as (bytes uint8[rows, cols], scale float32[rows])."""
-    import torch
-    ld = _matrix(x, "x")
-    rows, cols = x.shape
-    out = _out(out, "out", (rows, cols), torch.uint8, x.device)
-    scale = _out(scale, "scale", (rows,), torch.float32, x.device)
-    _launch(x.device, "hx_quantize_rows", lib().hx_quantize_rows, fmt, _dtype(x), x.data_ptr(), rows, cols, ld,
-            out.data_ptr(), scale.data_ptr())
+    torch = _torch or _load_torch()
+    dev = _device(x, "x")
+    dt = _dtype(x)
+    rows, cols, ld = _matrix(x, "x")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        ob = out.data_ptr()
+    else:
+        ob = _dense(out, "out", (rows, cols), torch.uint8, dev)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        sp = scale.data_ptr()
+    else:
+        sp = _dense(scale, "scale", (rows,), torch.float32, dev)
+    _launch(dev, "hx_quantize_rows", lib().hx_quantize_rows, fmt, dt, x.data_ptr(), rows, cols, ld, ob, sp)
     return out, scale
 
 
 def dequantize_rows(data, scale, fmt: int = ROWS_E4M3, dtype=None, out=None):
     """hx_dequantize_rows: the values of 8-bit rows, as `dtype` (default bfloat16) or into the matrix `out`."""
-    import torch
-    _cuda(data, "bytes")
-    if data.dim() != 2:
+    torch = _torch or _load_torch()
+    dev = _device(data, "bytes")
+    shape = data.shape
+    if len(shape) != 2:
         raise ValueError("bytes must be a matrix")
-    _rows8(data, scale, tuple(data.shape), data.device)
+    db = _dense(data, "bytes", shape, torch.uint8, dev)
+    sp = _dense(scale, "scale", shape[:1], torch.float32, dev)
     if out is None:
-        out = torch.empty(data.shape, dtype=dtype or torch.bfloat16, device=data.device)
-    ld = _matrix(out, "out", data.shape, dtype, data.device)
-    _launch(data.device, "hx_dequantize_rows", lib().hx_dequantize_rows, fmt, _dtype(out), data.data_ptr(),
-            scale.data_ptr(), data.shape[0], data.shape[1], out.data_ptr(), ld)
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=data.device)
+    else:
+        _same(out, "out", shape, dtype or out.dtype, dev)
+    rows, cols, ld = _matrix(out, "out")
+    _launch(dev, "hx_dequantize_rows", lib().hx_dequantize_rows, fmt, _dtype(out), db, sp, rows, cols, out.data_ptr(), ld)
     return out
 
 
 def gated_forward(x, fmt: int = ROWS_E4M3, save: bool = True, out=None):
     """hx_gated_forward: silu(gate) * up of x [rows, 2 cols] (gate first). Returns (h, bytes uint8[rows, 2,
     cols], scale float32[rows, 2]); with save=False (h, None, None)."""
-    import torch
-    ld = _matrix(x, "x")
-    rows, cols = x.shape[0], x.shape[1] // 2
-    if x.shape[1] % 2:
+    torch = _torch or _load_torch()
+    dev = _device(x, "x")
+    dt = _dtype(x)
+    rows, both, ld = _matrix(x, "x")
+    cols = both // 2
+    if both % 2:
         raise ValueError("x must have as many gate columns as up columns")
-    out = _out(out, "out", (rows, cols), x.dtype, x.device)
-    data = scale = None
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", (rows, cols), x.dtype, dev)
+    data = scale = db = sp = None
     if save:
-        data = torch.empty(rows, 2, cols, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(rows, 2, dtype=torch.float32, device=x.device)
-    _launch(x.device, "hx_gated_forward", lib().hx_gated_forward, fmt, _dtype(x), x.data_ptr(), rows, cols, ld,
-            out.data_ptr(), data.data_ptr() if save else None, scale.data_ptr() if save else None)
+        data = torch.empty((rows, 2, cols), dtype=torch.uint8, device=x.device)
+        scale = torch.empty((rows, 2), dtype=torch.float32, device=x.device)
+        db, sp = data.data_ptr(), scale.data_ptr()
+    _launch(dev, "hx_gated_forward", lib().hx_gated_forward, fmt, dt, x.data_ptr(), rows, cols, ld, op, db, sp)
     return out, data, scale
 
 
 def gated_backward(dh, data, scale, fmt: int = ROWS_E4M3, need_h: bool = False):
     """hx_gated_backward: (gradient of x [rows, 2 cols], the activation h again or None) for the gradient dh of
     gated_forward's output, at the saved gate and up."""
-    import torch
-    ld = _matrix(dh, "dh")
-    rows, cols = dh.shape
-    _rows8(data, scale, (rows, 2, cols), dh.device)
-    dx = torch.empty(rows, 2 * cols, dtype=dh.dtype, device=dh.device)
-    h = torch.empty(rows, cols, dtype=dh.dtype, device=dh.device) if need_h else None
-    _launch(dh.device, "hx_gated_backward", lib().hx_gated_backward, fmt, _dtype(dh), dh.data_ptr(), ld,
-            data.data_ptr(), scale.data_ptr(), rows, cols, dx.data_ptr(), h.data_ptr() if need_h else None)
+    torch = _torch or _load_torch()
+    dev = _device(dh, "dh")
+    dt = _dtype(dh)
+    rows, cols, ld = _matrix(dh, "dh")
+    db = _dense(data, "bytes", (rows, 2, cols), torch.uint8, dev)
+    sp = _dense(scale, "scale", (rows, 2), torch.float32, dev)
+    dx = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dh.device)
+    h = torch.empty((rows, cols), dtype=dh.dtype, device=dh.device) if need_h else None
+    _launch(dev, "hx_gated_backward", lib().hx_gated_backward, fmt, dt, dh.data_ptr(), ld, db, sp, rows, cols,
+            dx.data_ptr(), h.data_ptr() if need_h else None)
     return dx, h
 
 
-def _heads(t, what, shape=None, dtype=None, device=None):
+def _heads(t, what):
     """Token and head strides of [tokens, heads, dim] whose heads are contiguous."""
-    _cuda(t, what, shape, dtype, device)
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1 and t.numel()):
+    stride = t.stride()
+    if len(stride) != 3 or (stride[2] != 1 and t.shape[2] > 1 and t.numel()):
         raise ValueError(f"{what} must be [tokens, heads, dim] with contiguous heads")
-    return t.stride(0), t.stride(1)
+    return stride[0], stride[1]
 
 
-def _heads_out(t, shape, dtype, device):
+def _heads_out(t, shape, dtype, dev):
     """As _heads, for an output: two of its heads may not overlap."""
-    a, b = _heads(t, "out", shape, dtype, device)
-    tokens, heads, dim = shape
-    inner = min((s, n) for s, n in ((a, tokens), (b, heads)) if n > 1) if max(tokens, heads) > 1 else (dim, 1)
-    outer = max(s for s, n in ((a, tokens), (b, heads), (dim, 2)) if n > 1)
-    if not t.numel():
-        return a, b
-    if inner[0] < dim or (min(tokens, heads) > 1 and outer < inner[0] * (inner[1] - 1) + dim):
-        raise ValueError("out must not overlap itself")
+    _same(t, "out", shape, dtype, dev)
+    a, b = _heads(t, "out")
+    if t.numel():
+        # the shorter stride clears a head, the longer one everything under it
+        at = sorted((s, n) for s, n in ((a, shape[0]), (b, shape[1])) if n > 1)
+        span = shape[2]
+        for s, n in at:
+            if s < span:
+                raise ValueError("out must not overlap itself")
+            span = s * (n - 1) + span
     return a, b
 
 
-def _head_norm_rope(t, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt):
-    import torch
+# hx_head_norm_rope, field by field
+_NORM = struct.Struct("@IIIIQIIIIIfQPPPPP")
+
+
+def _head_norm_rope(t, dev, dt, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt):
+    torch = _torch
     tokens, heads, dim = t.shape
-    dev = t.device
     if not 0 <= q_heads <= heads:
         raise ValueError("q_heads must be between 0 and the number of heads")
-    w = wq if wq is not None else wk
-    if (q_heads and wq is None) or (q_heads < heads and wk is None) or w is None:
+    w = wk if wq is None else wq
+    if w is None or (q_heads and wq is None) or (q_heads < heads and wk is None):
         raise ValueError("a weight is missing")
-    for name, v in (("wq", wq), ("wk", wk)):
-        if v is not None:
-            _cuda(v, name, (dim,), w.dtype, dev)
-            if not v.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    _cuda(cos, "cos", None, torch.float32, dev)
-    _cuda(sin, "sin", cos.shape, torch.float32, dev)
-    if cos.dim() != 2 or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous [places, rot_dim / 2]")
-    _cuda(positions, "positions", (tokens,), None, dev)
-    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous():
-        raise TypeError("positions must be contiguous int64 or int32")
-    return _HeadNormRope(fmt, _dtype(t), _dtype(w), 64 if positions.dtype is torch.int64 else 32, tokens, q_heads,
-                         heads - q_heads, dim, 2 * cos.shape[1], bool(interleaved), eps, cos.shape[0],
-                         wq.data_ptr() if wq is not None else None, wk.data_ptr() if wk is not None else None,
-                         cos.data_ptr(), sin.data_ptr(), positions.data_ptr())
+    _device(w, "a weight")
+    wp = 0 if wq is None else _dense(wq, "wq", (dim,), w.dtype, dev)
+    kp = 0 if wk is None else _dense(wk, "wk", (dim,), w.dtype, dev)
+    _device(cos, "cos")
+    table = cos.shape
+    if len(table) != 2:
+        raise ValueError("cos and sin must be [places, rot_dim / 2]")
+    cp = _dense(cos, "cos", table, torch.float32, dev)
+    sp = _dense(sin, "sin", table, torch.float32, dev)
+    _device(positions, "positions")
+    long = positions.dtype is torch.int64
+    pp = _dense(positions, "positions", (tokens,), torch.int64 if long else torch.int32, dev)
+    return _NORM.pack(fmt, dt, _dtype(w), 64 if long else 32, tokens, q_heads, heads - q_heads, dim, 2 * table[1],
+                      1 if interleaved else 0, eps, table[0], wp, kp, cp, sp, pp)
 
 
 def head_norm_rope_forward(x, q_heads: int, wq, wk, cos, sin, positions, eps: float = 1e-6,
@@ -707,20 +726,24 @@ def head_norm_rope_forward(x, q_heads: int, wq, wk, cos, sin, positions, eps: fl
     rotation of its first 2 * cos.shape[1] values by row positions[t] of cos and sin. Returns (y, bytes
     uint8[tokens, heads, dim], scale float32[tokens, heads]); with save=False (y, None, None). `out` may
     be x."""
-    import torch
+    torch = _torch or _load_torch()
+    dev = _device(x, "x")
+    dt = _dtype(x)
     xt, xh = _heads(x, "x")
-    p = _head_norm_rope(x, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
-    dev = x.device
+    p = _head_norm_rope(x, dev, dt, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
+    shape = x.shape
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    yt, yh = _heads_out(out, x.shape, x.dtype, dev)
-    data = scale = None
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        yt, yh = out.stride()[:2]
+    else:
+        yt, yh = _heads_out(out, shape, x.dtype, dev)
+    data = scale = db = sp = None
     if save:
-        data = torch.empty(x.shape, dtype=torch.uint8, device=dev)
-        scale = torch.empty(x.shape[:2], dtype=torch.float32, device=dev)
-    _launch(dev, "hx_head_norm_rope_forward", lib().hx_head_norm_rope_forward, ctypes.byref(p), x.data_ptr(), xt, xh,
-            out.data_ptr(), yt, yh, data.data_ptr() if save else None, scale.data_ptr() if save else None,
-            _status_ptr(status, dev))
+        data = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(shape[:2], dtype=torch.float32, device=x.device)
+        db, sp = data.data_ptr(), scale.data_ptr()
+    _launch(dev, "hx_head_norm_rope_forward", lib().hx_head_norm_rope_forward, p, x.data_ptr(), xt, xh, out.data_ptr(),
+            yt, yh, db, sp, _status_ptr(status, dev))
     return out, data, scale
 
 
@@ -728,21 +751,28 @@ def head_norm_rope_backward(dy, data, scale, q_heads: int, wq, wk, cos, sin, pos
                             interleaved: bool = False, fmt: int = ROWS_E4M3, out=None, status=None):
     """hx_head_norm_rope_backward: (dx, dwq, dwk) at the saved x; the weights' gradients are float32 (None for a
     weight that is None). `out` (dx) may be dy."""
-    import torch
-    dt, dh = _heads(dy, "dy")
-    p = _head_norm_rope(dy, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
-    dev = dy.device
-    _rows8(data, scale, tuple(dy.shape), dev)
+    torch = _torch or _load_torch()
+    dev = _device(dy, "dy")
+    dt = _dtype(dy)
+    gt, gh = _heads(dy, "dy")
+    p = _head_norm_rope(dy, dev, dt, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
+    shape = dy.shape
+    db = _dense(data, "bytes", shape, torch.uint8, dev)
+    sp = _dense(scale, "scale", shape[:2], torch.float32, dev)
     if out is None:
-        out = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
-    ot, oh = _heads_out(out, dy.shape, dy.dtype, dev)
-    dim = dy.shape[2]
-    ws = torch.empty(lib().hx_head_norm_rope_workspace(dim), dtype=torch.uint8, device=dev)
-    dwq = torch.empty(dim, dtype=torch.float32, device=dev) if wq is not None else None
-    dwk = torch.empty(dim, dtype=torch.float32, device=dev) if wk is not None else None
-    _launch(dev, "hx_head_norm_rope_backward", lib().hx_head_norm_rope_backward, ctypes.byref(p), dy.data_ptr(), dt, dh,
-            data.data_ptr(), scale.data_ptr(), out.data_ptr(), ot, oh, dwq.data_ptr() if dwq is not None else None,
-            dwk.data_ptr() if dwk is not None else None, ws.data_ptr(), ws.numel(), _status_ptr(status, dev))
+        out = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        ot, oh = out.stride()[:2]
+    else:
+        ot, oh = _heads_out(out, shape, dy.dtype, dev)
+    dim = shape[2]
+    fn = lib()
+    need = fn.hx_head_norm_rope_workspace(dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    dwq = torch.empty(dim, dtype=torch.float32, device=dy.device) if wq is not None else None
+    dwk = torch.empty(dim, dtype=torch.float32, device=dy.device) if wk is not None else None
+    _launch(dev, "hx_head_norm_rope_backward", fn.hx_head_norm_rope_backward, p, dy.data_ptr(), gt, gh, db, sp,
+            out.data_ptr(), ot, oh, dwq.data_ptr() if dwq is not None else None,
+            dwk.data_ptr() if dwk is not None else None, ws.data_ptr(), need, _status_ptr(status, dev))
     return out, dwq, dwk
 
 
@@ -751,23 +781,26 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     """hx_weight_grad: dY^T X [n_out, n_in] of a linear layer, from dy [tokens, n_out] (float16 or bfloat16) and the
     8-bit rows of its input X [tokens, n_in]. The result has `dtype` (dy's, or float32), or goes to the
     matrix `out`, onto its old values if `accumulate`."""
-    import torch
-    ld = _matrix(dy, "dy")
-    tokens, n_out = dy.shape
-    dev = dy.device
-    _cuda(data, "bytes", None, torch.uint8, dev)
-    if data.dim() != 2 or data.shape[0] != tokens:
+    torch = _torch or _load_torch()
+    dev = _device(dy, "dy")
+    dt = _dtype(dy)
+    tokens, n_out, ld = _matrix(dy, "dy")
+    _device(data, "bytes")
+    if data.dim() != 2:
         raise ValueError("bytes must be [tokens, n_in]")
     n_in = data.shape[1]
-    _rows8(data, scale, (tokens, n_in), dev)
+    db = _dense(data, "bytes", (tokens, n_in), torch.uint8, dev)
+    sp = _dense(scale, "scale", (tokens,), torch.float32, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(n_out, n_in, dtype=dtype or dy.dtype, device=dev)
-    ldw = _matrix(out, "out", (n_out, n_in), dtype, dev)
-    need = lib().hx_weight_grad_workspace(tokens, n_out, n_in)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _launch(dev, "hx_weight_grad", lib().hx_weight_grad, fmt, _dtype(dy), dy.data_ptr(), ld, data.data_ptr(),
-            scale.data_ptr(), tokens, n_out, n_in, _dtype(out), out.data_ptr(), ldw, int(accumulate),
-            ws.data_ptr() if need else None, need, _status_ptr(status, dev))
+        out = torch.empty((n_out, n_in), dtype=dtype or dy.dtype, device=dy.device)
+    else:
+        _same(out, "out", (n_out, n_in), dtype or out.dtype, dev)
+    ldw = _matrix(out, "out")[2]
+    fn = lib()
+    need = fn.hx_weight_grad_workspace(tokens, n_out, n_in)
+    ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, dy.data_ptr(), ld, db, sp, tokens, n_out, n_in, _dtype(out),
+            out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
     return out

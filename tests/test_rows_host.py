@@ -121,6 +121,14 @@ def test_head_norm_rope_refusals(kw):
     assert L.hx_head_norm_rope_backward(_norm(**kw), A, 384, 64, A, A, A, 384, 64, A, A, A, n, None, None) == bad
 
 
+def test_head_norm_rope_fields():
+    """The binding's packed arguments have the layout of the C structure."""
+    v = (0, 2, 0, 64, 4, 4, 2, 64, 32, 1, 0.5, 16, A, A + 8, A + 16, A + 24, A + 32)
+    p = hx._HeadNormRope.from_buffer_copy(hx._NORM.pack(*v))
+    assert ctypes.sizeof(p) == hx._NORM.size
+    assert tuple(getattr(p, n) for n, _ in p._fields_) == v
+
+
 def test_head_norm_rope_call_refusals():
     L, bad = hx.lib(), hx.HX_ERR_ARG
     f, b = L.hx_head_norm_rope_forward, L.hx_head_norm_rope_backward
