@@ -4,11 +4,11 @@
 // A product of two matrices whose contraction runs over the tokens, so both operands are stored with
 // the contraction outermost (MN-major). Tensor cores: tcgen05.mma, accumulators in TMEM, one CTA
 // per tile of BM output by BN input features, steps of 64 tokens.
-//   warps 0-15  read the bytes (8 columns of a token per lane, the next steps' already in flight),
+//   warps 0 ..  read the bytes (8 columns of a token per lane, the next steps' already in flight),
 //               turn them into s_t q in dY's type and write them to shared memory in the 128-byte
 //               swizzle that the tensor core reads; at the end they read TMEM and store the tile.
-//   warp 16     brings dY's tile by TMA, in the same swizzle.
-//   warp 17     issues the products.
+//   one warp    brings dY's tile by TMA, in the same swizzle.
+//   one warp    issues the products.
 // The bytes never exist as a 16-bit matrix in memory. s_t q in bf16 is exact for e4m3 (the scale is a
 // power of two). For INT8 it is not, and one rounding to bf16 would put an error of the size of the result's
 // own rounding into every product: there the tile is held as two, the rounded values and the rounded
@@ -33,9 +33,6 @@ namespace {
 using namespace hxv;
 
 constexpr int kStep = 64;             // tokens per pipeline stage
-constexpr int kWarps = 16;            // converting warps
-constexpr int kTokens = kStep / kWarps;  // a converting warp's tokens of a stage
-constexpr int kThreads = 32 * (kWarps + 2);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxSplits = 32;
 
@@ -142,9 +139,17 @@ struct Tile {
   static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;
   static constexpr int kStage = kA + kParts * kB;
   static constexpr int kStages = 196608 / kStage;
+  // Groups of converting warps: group g takes steps g, g + kGroups, ... Not more than stages: a group then
+  // comes to a stage's next use only after the use before last has been released, which a wait for one
+  // bit of phase relies on.
+  static constexpr int kGroups = kStages < 4 ? kStages : 4;
+  static constexpr int kGroupWarps = kGroups == 2 ? 8 : 4;
+  static constexpr int kWarps = kGroups * kGroupWarps;
+  static constexpr int kTokens = kStep / kGroupWarps;  // a converting warp's tokens of its step
+  static constexpr int kThreads = 32 * (kWarps + 2);
   static constexpr int kCols = MT * NT;  // TMEM columns: a power of two of at least 32
   static constexpr int kSmem = kStages * kStage + 1024;
-  static_assert(kStages >= 2 && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
+  static_assert(kStages >= 2 && kGroups <= kStages && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
 };
 
 struct Barriers {
@@ -243,9 +248,10 @@ __device__ __forceinline__ void store_tile(const Args& a, uint32_t row, uint32_t
 }
 
 template <typename T, int MT, int NT, int kParts, bool kTma>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const Args a) {
   using S = Tile<MT, NT, kParts>;
+  constexpr int kGroups = S::kGroups, kGroupWarps = S::kGroupWarps, kWarps = S::kWarps, kTokens = S::kTokens;
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bars;
   const uint32_t tiles = (smem_addr(raw) + 1023u) & ~1023u;
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       bar_init(copied(s), 1);
-      bar_init(converted(s), kWarps);
+      bar_init(converted(s), kGroupWarps);
       bar_init(empty(s), 1);
     }
     bar_init(done, 1);
@@ -281,71 +287,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
 
   if (warp < kWarps) {
-    // ---- converting warps: tokens kTokens * warp .. of every step
+    // ---- converting warps. A step's chain (wait, convert, store, fence, arrive) is longer than its products
+    // take, so the groups work on two to four steps at once, and a group's next bytes have the others' steps to
+    // arrive.
     // 8 columns per lane: a warp's load is one token's 256 columns, or two tokens' 128 (lanes
     // 16-31 the odd one). Lanes 8 i .. 8 i + 7 write one whole line, so no two share a bank.
     static_assert(NT == 256 || NT == 128, "");
     constexpr int kLoads = NT == 256 ? kTokens : kTokens / 2;
-    Bytes<8> b[2][kLoads];
-    float sc[2];
-    auto token_of = [&](int j) { return NT == 256 ? j : 2 * j + (int)(lane >> 4); };
-    auto fetch = [&](uint32_t k, int buf) {
-      const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * kTokens;
-      const uint32_t c = n0 + (NT == 256 ? lane : lane & 15) * 8;
+    const uint32_t group = warp / kGroupWarps, line0 = warp % kGroupWarps * kTokens;
+    const uint32_t ch = NT == 256 ? lane : lane & 15;  // the lane's chunk of 8 columns
+    const uint32_t odd = NT == 256 ? 0 : lane >> 4;
+    auto token_of = [&](int j) { return NT == 256 ? (uint32_t)j : 2 * j + odd; };
+    Bytes<8> b[kLoads];
+    float sc = 0.0f;
+    const uint8_t* at = a.bytes + ((uint64_t)(k0 + group) * kStep + line0 + odd) * a.n_in + n0 + ch * 8;
+    auto fetch = [&](uint32_t k) {
+      const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
+      sc = 0.0f;
+      if (k < steps && t + (lane & (kTokens - 1)) < a.tokens) sc = a.scale[t + (lane & (kTokens - 1))];
+      if (a.x_wide && n0 + NT <= a.n_in && k < steps && t + kTokens <= a.tokens) {
+        const uint8_t* p = at;
+        const uint32_t step = NT == 256 ? a.n_in : 2 * a.n_in;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) b[buf][j] = fetch_bytes(a, k < steps ? t + token_of(j) : a.tokens, c);
-      sc[buf] = 0.0f;
-      if (k < steps && t + (lane & (kTokens - 1)) < a.tokens) sc[buf] = a.scale[t + (lane & (kTokens - 1))];
+        for (int j = 0; j < kLoads; ++j, p += step) b[j].load(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) b[j] = fetch_bytes(a, k < steps ? t + token_of(j) : a.tokens, n0 + ch * 8);
+      }
+      at += (uint64_t)kGroups * kStep * a.n_in;
     };
-    auto one = [&](uint32_t k, int buf) {
+    fetch(group);
+    bool ok = true;
+    for (uint32_t k = group; k < steps; k += kGroups) {
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
-      if (!__all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed))) return false;
+      if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)))) break;
       const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int tk = token_of(j);
-        const float f = __shfl_sync(0xffffffffu, sc[buf], tk);
-        const uint32_t ch = NT == 256 ? lane : lane & 15, line = warp * kTokens + tk;
+        const uint32_t line = line0 + token_of(j);
+        const float f = __shfl_sync(0xffffffffu, sc, token_of(j));
         uint4 v[kParts];
-        convert<T, kParts>(a.fmt, b[buf][j], f, v);
+        convert<T, kParts>(a.fmt, b[j], f, v);
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
           put(B + p * S::kB + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), v[p]);
       }
       if constexpr (!kTma) {
-        const uint64_t t = (uint64_t)(k0 + k) * kStep + warp * kTokens;
+        const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
         for (int h = 0; h < S::BM; h += 256)
           for (int j = 0; j < kTokens; ++j) {
-            const uint32_t ch = h / 8 + lane, line = warp * kTokens + j;
-            if (ch * 8 < S::BM)
-              put(A + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), fetch_dy<T>(a, t + j, m0 + ch * 8));
+            const uint32_t c = h / 8 + lane, line = line0 + j;
+            if (c * 8 < S::BM)
+              put(A + (c >> 3) * 8192 + line * 128 + (((c ^ line) & 7) << 4), fetch_dy<T>(a, t + j, m0 + c * 8));
           }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(converted(s));
-      return true;
-    };
-    fetch(0, 0);
-    fetch(1, 1);
-    bool ok = true;
-    for (uint32_t k = 0; k < steps; k += 2) {
-      if (!(ok = one(k, 0))) break;
-      fetch(k + 2, 0);
-      if (k + 1 >= steps) break;
-      if (!(ok = one(k + 1, 1))) break;
-      fetch(k + 3, 1);
+      fetch(k + kGroups);
     }
     // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
     if (ok && steps) ok = bar_wait(done, 0, failed);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (__all_sync(0xffffffffu, ok)) {
-      const uint32_t mt = (warp >> 2) % MT;
-      constexpr uint32_t kWidth = NT * 4 * MT / kWarps;  // columns per warp
-      const uint32_t c0 = (warp >> 2) / MT * kWidth, c1 = c0 + kWidth;
-      const uint32_t row = m0 + mt * 128 + (warp & 3) * 32 + lane;
-      for (uint32_t c = c0; c < c1; c += 32) {
+      // 32 columns at a time, the warps of a lane quarter in turn
+      for (uint32_t i = warp >> 2; i < MT * NT / 32; i += kWarps / 4) {
+        const uint32_t mt = i / (NT / 32), c = i % (NT / 32) * 32;
+        const uint32_t row = m0 + mt * 128 + (warp & 3) * 32 + lane;
         uint32_t r[32];
         if (steps) {
           tmem_load32(tmem + ((warp & 3) * 32 << 16) + mt * NT + c, r);
@@ -472,7 +481,7 @@ int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
     return HX_ERR_CUDA;
   const dim3 grid((a.n_out + S::BM - 1) / S::BM, (a.n_in + S::BN - 1) / S::BN, a.splits);
-  kernel<<<grid, kThreads, S::kSmem, s>>>(map, a);
+  kernel<<<grid, S::kThreads, S::kSmem, s>>>(map, a);
   return launched();
 }
 template <typename T, int MT, int NT>
