@@ -35,6 +35,7 @@ using namespace hxv;
 constexpr int kStep = 64;             // tokens per pipeline stage
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxSplits = 32;
+constexpr int kBand = 4;              // tile rows that are walked together
 
 struct Args {
   uint32_t fmt;
@@ -62,13 +63,33 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same on the barrier at this address in CTA `rank` of the cluster.
+__device__ __forceinline__ void bar_arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar), "r"(rank)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -103,21 +124,37 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
   constexpr uint64_t kBlock = 8192 >> 4, kAtom = 1024 >> 4;
   return (uint64_t)((addr & 0x3ffffu) >> 4) | kBlock << 16 | kAtom << 32 | 1ull << 46 | 2ull << 61;
 }
-template <typename T, int N>
+template <typename T, int M, int N>
 __device__ constexpr uint32_t instruction() {
   constexpr uint32_t type = sizeof(T) && Type<T>::kInf == 0x7f80u ? 1 : 0;  // bf16 or f16
-  return 1u << 4 | type << 7 | type << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N / 8) << 17 | (128u / 16) << 24;
+  return 1u << 4 | type << 7 | type << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N / 8) << 17 | (uint32_t)(M / 16) << 24;
 }
+template <bool kPair>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+        : "memory");
 }
+// Arrives on the barrier (of both CTAs of a pair) once the products issued so far are done.
+template <bool kPair>
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
@@ -133,23 +170,29 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-template <int MT, int NT, int kParts>
+// A CTA, or a pair of CTAs on two SMs of one cluster, per tile. MT accumulators of 128 rows per CTA; 128
+// columns of X in each CTA's shared memory. A pair's products take both CTAs' columns (the second CTA's
+// through the pair's own path): 256 columns, each converted and read from shared memory by one CTA only.
+template <int MT, bool kPair, int kParts>
 struct Tile {
-  static constexpr int BM = 128 * MT, BN = NT;
-  static constexpr int kA = BM * kStep * 2, kB = BN * kStep * 2;
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int M = 128 * kCtas, N = 128 * kCtas;  // of one product
+  static constexpr int BM = M * MT, BN = N;               // of the tile
+  static constexpr int kA = 128 * MT * kStep * 2, kB = 128 * kStep * 2;
   static constexpr int kStage = kA + kParts * kB;
-  static constexpr int kStages = 196608 / kStage;
+  static constexpr int kStages = 196608 / kStage < 8 ? 196608 / kStage : 8;
   // Groups of converting warps: group g takes steps g, g + kGroups, ... Not more than stages: a group then
   // comes to a stage's next use only after the use before last has been released, which a wait for one
   // bit of phase relies on.
   static constexpr int kGroups = kStages < 4 ? kStages : 4;
-  static constexpr int kGroupWarps = kGroups == 2 ? 8 : 4;
+  static constexpr int kGroupWarps = 4;
   static constexpr int kWarps = kGroups * kGroupWarps;
   static constexpr int kTokens = kStep / kGroupWarps;  // a converting warp's tokens of its step
   static constexpr int kThreads = 32 * (kWarps + 2);
-  static constexpr int kCols = MT * NT;  // TMEM columns: a power of two of at least 32
+  static constexpr int kCols = MT * N;  // TMEM columns: a power of two of at least 32
   static constexpr int kSmem = kStages * kStage + 1024;
-  static_assert(kStages >= 2 && kGroups <= kStages && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
+  static_assert(kStages * kStage >= kWarps * 4096, "");  // the epilogue's rows
+  static_assert(kStages >= 3 && kGroups <= kStages && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
 };
 
 struct Barriers {
@@ -217,46 +260,103 @@ __device__ __forceinline__ void put(uint32_t addr, const uint4& v) {
 }
 
 // ------------------------------------------------------------------------------------ the tile
+// A warp's 32 rows of C = 128 / sizeof(O) columns from TMEM (columns tm ..) to the matrix o (n_rows x n_cols, row
+// stride ld) at (row, col). The rows pass through 4 KB of shared memory, so that the stores are whole lines (a lane
+// per row straight from TMEM would touch 32 lines with each store).
 template <typename O>
-__device__ __forceinline__ void store_tile(const Args& a, uint32_t row, uint32_t col, const uint32_t (&r)[32]) {
-  O* o = static_cast<O*>(a.dw) + (uint64_t)row * a.ld_dw + col;
-  if (a.dw_wide && col + 32 <= a.n_in) {
+__device__ __forceinline__ void store_block(uint32_t stage, uint32_t tm, bool any, O* o, uint64_t ld, bool wide, bool add,
+                                            uint32_t row, uint32_t col, uint32_t n_rows, uint32_t n_cols) {
+  constexpr uint32_t C = 128 / sizeof(O);
+  const uint32_t lane = threadIdx.x & 31;
+  if (!add) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      float f[8];
+    for (uint32_t h = 0; h < C / 32; ++h) {
+      uint32_t r[32];
+      tmem_load32(tm + h * 32, r);
+      constexpr uint32_t kChunks = 32 * sizeof(O) / 16, kPer = 16 / sizeof(O);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[i + j]);
-      if (a.accumulate) {
-        Vec<O, 8> old;
-        old.load(o + i);
-        float g[8];
-        old.floats(g);
+      for (uint32_t c = 0; c < kChunks; ++c) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += g[j];
+        for (uint32_t i = 0; i < 4; ++i) {
+          if constexpr (sizeof(O) == 4)
+            w[i] = any ? r[4 * c + i] : 0;
+          else
+            w[i] = any ? pack2<O>(__uint_as_float(r[(kPer * c + 2 * i) % 32]), __uint_as_float(r[(kPer * c + 2 * i + 1) % 32])) : 0;
+        }
+        put(stage + lane * 128 + (((h * kChunks + c) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
       }
-      store<O, 8>(o + i, f);
     }
-  } else {
+    __syncwarp();
+    if (wide && col + C <= n_cols) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < a.n_in) {
-        float f = __uint_as_float(r[i]);
-        if (a.accumulate) f += Type<O>::to_f(o[i]);
-        o[i] = Type<O>::from_f(f);
+      for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t y = i * 4 + (lane >> 3), c = lane & 7;
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage + y * 128 + ((c ^ (y & 7)) << 4)));
+        if (row + y < n_rows) *reinterpret_cast<uint4*>(o + (uint64_t)(row + y) * ld + col + c * (16 / sizeof(O))) = v;
       }
+    } else {
+      for (uint32_t y = 0; y < 32 && row + y < n_rows; ++y)
+#pragma unroll
+        for (uint32_t h = 0; h < C / 32; ++h) {
+          const uint32_t x = h * 32 + lane, byte = x * sizeof(O);
+          const uint32_t at = stage + y * 128 + (((byte >> 4) ^ (y & 7)) << 4) + (byte & 15);
+          O* p = o + (uint64_t)(row + y) * ld + col + x;
+          if constexpr (sizeof(O) == 4) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+            if (col + x < n_cols) *reinterpret_cast<uint32_t*>(p) = v;
+          } else {
+            uint16_t v;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at));
+            if (col + x < n_cols) *reinterpret_cast<uint16_t*>(p) = v;
+          }
+        }
+    }
+    __syncwarp();
+  } else {
+    // onto old values: 32-bit sums through shared memory, 32 columns at a time, so that the total rounds once
+    for (uint32_t h = 0; h < C / 32; ++h) {
+      uint32_t r[32];
+      tmem_load32(tm + h * 32, r);
+#pragma unroll
+      for (uint32_t c = 0; c < 8; ++c)
+        put(stage + lane * 128 + ((c ^ (lane & 7)) << 4),
+            any ? make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]) : make_uint4(0, 0, 0, 0));
+      __syncwarp();
+      const uint32_t x = col + h * 32 + lane;
+      for (uint32_t y = 0; y < 32 && row + y < n_rows; ++y) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(stage + y * 128 + (((lane >> 2) ^ (y & 7)) << 4) + (lane & 3) * 4));
+        O* p = o + (uint64_t)(row + y) * ld + x;
+        if (x < n_cols) *p = Type<O>::from_f(Type<O>::to_f(*p) + v);
+      }
+      __syncwarp();
+    }
   }
 }
 
-template <typename T, int MT, int NT, int kParts, bool kTma>
-__global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
-    k_wgrad(const __grid_constant__ CUtensorMap map, const Args a) {
-  using S = Tile<MT, NT, kParts>;
+template <typename T, int MT, bool kPair, int kParts, bool kTma>
+__global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a) {
+  using S = Tile<MT, kPair, kParts>;
   constexpr int kGroups = S::kGroups, kGroupWarps = S::kGroupWarps, kWarps = S::kWarps, kTokens = S::kTokens;
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bars;
   const uint32_t tiles = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t m0 = blockIdx.x * S::BM, n0 = blockIdx.y * S::BN, split = blockIdx.z;
+  const uint32_t rank = kPair ? cluster_rank() : 0;
+  // Tiles in bands of kBand tile rows, columns slowest within a band: what runs at once shares 4 tiles' worth of
+  // dY and about 18 of X, whose bytes are the smaller (a tile's dY takes four times its X from memory).
+  const uint32_t tile = blockIdx.x / S::kCtas, rows = (a.n_out + S::BM - 1) / S::BM, cols = (a.n_in + S::BN - 1) / S::BN;
+  const uint32_t band = tile / (kBand * cols), in_band = tile - band * kBand * cols;
+  const uint32_t high = min((uint32_t)kBand, rows - band * kBand);
+  const uint32_t m0 = (band * kBand + in_band % high) * S::BM + rank * 128;  // accumulator i: rows m0 + i * M ..
+  const uint32_t n0 = in_band / high * S::BN, x0 = n0 + rank * 128;          // the tile's columns, the CTA's
+  const uint32_t split = blockIdx.y;
   const uint32_t per = (a.steps + a.splits - 1) / a.splits;
   const uint32_t k0 = min(split * per, a.steps), k1 = min(k0 + per, a.steps), steps = k1 - k0;
   volatile uint32_t* failed = &bars.failed;
@@ -268,7 +368,7 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       bar_init(copied(s), 1);
-      bar_init(converted(s), kGroupWarps);
+      bar_init(converted(s), S::kCtas * kGroupWarps);  // (of a pair: the first CTA's, for both)
       bar_init(empty(s), 1);
     }
     bar_init(done, 1);
@@ -276,43 +376,50 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarps + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
-                 "r"((uint32_t)S::kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
+                   "r"((uint32_t)S::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
+                   "r"((uint32_t)S::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if constexpr (kPair)
+    cluster_sync();
+  else
+    __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
 
   if (warp < kWarps) {
     // ---- converting warps. A step's chain (wait, convert, store, fence, arrive) is longer than its products
-    // take, so the groups work on two to four steps at once, and a group's next bytes have the others' steps to
-    // arrive.
-    // 8 columns per lane: a warp's load is one token's 256 columns, or two tokens' 128 (lanes
-    // 16-31 the odd one). Lanes 8 i .. 8 i + 7 write one whole line, so no two share a bank.
-    static_assert(NT == 256 || NT == 128, "");
-    constexpr int kLoads = NT == 256 ? kTokens : kTokens / 2;
+    // take, so the groups work on three or four steps at once, and a group's next bytes have the others'
+    // steps to arrive. 8 columns per lane: a warp's load is two tokens' 128 columns (lanes 16-31 the odd
+    // one). Lanes 8 i .. 8 i + 7 write one whole line, so no two share a bank.
+    constexpr int kLoads = kTokens / 2;
     const uint32_t group = warp / kGroupWarps, line0 = warp % kGroupWarps * kTokens;
-    const uint32_t ch = NT == 256 ? lane : lane & 15;  // the lane's chunk of 8 columns
-    const uint32_t odd = NT == 256 ? 0 : lane >> 4;
-    auto token_of = [&](int j) { return NT == 256 ? (uint32_t)j : 2 * j + odd; };
+    const uint32_t ch = lane & 15, odd = lane >> 4;
     Bytes<8> b[kLoads];
     float sc = 0.0f;
-    const uint8_t* at = a.bytes + ((uint64_t)(k0 + group) * kStep + line0 + odd) * a.n_in + n0 + ch * 8;
+    const uint8_t* at = a.bytes + ((uint64_t)(k0 + group) * kStep + line0 + odd) * a.n_in + x0 + ch * 8;
     auto fetch = [&](uint32_t k) {
       const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
       sc = 0.0f;
       if (k < steps && t + (lane & (kTokens - 1)) < a.tokens) sc = a.scale[t + (lane & (kTokens - 1))];
-      if (a.x_wide && n0 + NT <= a.n_in && k < steps && t + kTokens <= a.tokens) {
+      if (a.x_wide && x0 + 128 <= a.n_in && k < steps && t + kTokens <= a.tokens) {
         const uint8_t* p = at;
-        const uint32_t step = NT == 256 ? a.n_in : 2 * a.n_in;
+        const uint64_t step = 2 * (uint64_t)a.n_in;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j, p += step) b[j].load(p);
       } else {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) b[j] = fetch_bytes(a, k < steps ? t + token_of(j) : a.tokens, n0 + ch * 8);
+        for (int j = 0; j < kLoads; ++j)
+          b[j] = fetch_bytes(a, k < steps ? t + 2 * j + odd : a.tokens, x0 + ch * 8);
       }
       at += (uint64_t)kGroups * kStep * a.n_in;
     };
@@ -325,8 +432,8 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
       const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const uint32_t line = line0 + token_of(j);
-        const float f = __shfl_sync(0xffffffffu, sc, token_of(j));
+        const uint32_t tk = 2 * j + odd, line = line0 + tk;
+        const float f = __shfl_sync(0xffffffffu, sc, tk);
         uint4 v[kParts];
         convert<T, kParts>(a.fmt, b[j], f, v);
 #pragma unroll
@@ -335,48 +442,45 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
       }
       if constexpr (!kTma) {
         const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
-        for (int h = 0; h < S::BM; h += 256)
-          for (int j = 0; j < kTokens; ++j) {
-            const uint32_t c = h / 8 + lane, line = line0 + j;
-            if (c * 8 < S::BM)
-              put(A + (c >> 3) * 8192 + line * 128 + (((c ^ line) & 7) << 4), fetch_dy<T>(a, t + j, m0 + c * 8));
+        for (int i = 0; i < MT; ++i)
+          for (int j = 0; j < kTokens; j += 2) {
+            const uint32_t line = line0 + j + odd;
+            put(A + i * 16384 + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4),
+                fetch_dy<T>(a, t + j + odd, m0 + i * S::M + ch * 8));
           }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(converted(s));
+      if (lane == 0) {
+        if constexpr (kPair)
+          bar_arrive_at(converted(s), 0);
+        else
+          bar_arrive(converted(s));
+      }
       fetch(k + kGroups);
     }
     // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
     if (ok && steps) ok = bar_wait(done, 0, failed);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (__all_sync(0xffffffffu, ok)) {
-      // 32 columns at a time, the warps of a lane quarter in turn
-      for (uint32_t i = warp >> 2; i < MT * NT / 32; i += kWarps / 4) {
-        const uint32_t mt = i / (NT / 32), c = i % (NT / 32) * 32;
-        const uint32_t row = m0 + mt * 128 + (warp & 3) * 32 + lane;
-        uint32_t r[32];
-        if (steps) {
-          tmem_load32(tmem + ((warp & 3) * 32 << 16) + mt * NT + c, r);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0;
-        }
-        if (row >= a.n_out || n0 + c >= a.n_in) {
-          // nothing of the matrix here
-        } else if (a.splits > 1) {
-          Args p = a;
-          p.dw = a.part + (uint64_t)split * a.n_out * a.n_in;
-          p.ld_dw = a.n_in;
-          p.accumulate = 0;
-          p.dw_wide = a.n_in % 4 == 0;
-          store_tile<float>(p, row, n0 + c, r);
-        } else if (a.dw_dtype == HX_F32) {
-          store_tile<float>(a, row, n0 + c, r);
-        } else {
-          store_tile<T>(a, row, n0 + c, r);
-        }
-        __syncwarp();
+      // a block of columns at a time, the warps of a lane quarter in turn; the stages are free by now
+      const uint32_t stage = tiles + warp * 4096;
+      const bool part = a.splits > 1;
+      const uint32_t width = part || a.dw_dtype == HX_F32 ? 32 : 64;
+      for (uint32_t i = warp >> 2; i < MT * S::N / width; i += kWarps / 4) {
+        const uint32_t mt = i / (S::N / width), c = i % (S::N / width) * width;
+        const uint32_t row = m0 + mt * S::M + (warp & 3) * 32, col = n0 + c;
+        const uint32_t tm = tmem + ((warp & 3) * 32 << 16) + mt * S::N + c;
+        if (row >= a.n_out || col >= a.n_in) continue;
+        if (part)
+          store_block<float>(stage, tm, steps > 0, a.part + (uint64_t)split * a.n_out * a.n_in, a.n_in, a.n_in % 4 == 0, false,
+                             row, col, a.n_out, a.n_in);
+        else if (a.dw_dtype == HX_F32)
+          store_block<float>(stage, tm, steps > 0, static_cast<float*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col,
+                             a.n_out, a.n_in);
+        else
+          store_block<T>(stage, tm, steps > 0, static_cast<T*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col, a.n_out,
+                         a.n_in);
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -386,23 +490,35 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
       for (; k < steps; ++k) {
         const uint32_t s = k % S::kStages;
         if (!bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)) break;
-        bar_expect(copied(s), S::kA);
         const int32_t t = (int32_t)((k0 + k) * kStep);
-        for (int i = 0; i < S::BM / 64; ++i)
-          asm volatile(
-              "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                  tiles + s * S::kStage + i * 8192),
-              "l"(&map), "r"((int32_t)(m0 + i * 64)), "r"(t), "r"(copied(s))
-              : "memory");
+        if constexpr (kPair) {
+          // both CTAs' copies count on the first one's barrier
+          if (rank == 0) bar_expect(copied(s), 2 * S::kA);
+          const uint32_t bar = at_rank(copied(s), 0);
+          for (int i = 0; i < 2 * MT; ++i)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                    tiles + s * S::kStage + i * 8192),
+                "l"(&map), "r"((int32_t)(m0 + i / 2 * S::M + i % 2 * 64)), "r"(t), "r"(bar)
+                : "memory");
+        } else {
+          bar_expect(copied(s), S::kA);
+          for (int i = 0; i < 2 * MT; ++i)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                    tiles + s * S::kStage + i * 8192),
+                "l"(&map), "r"((int32_t)(m0 + i / 2 * S::M + i % 2 * 64)), "r"(t), "r"(copied(s))
+                : "memory");
+        }
       }
-      if (k < steps) {  // gave up: wait for the copies already on their way
+      if (k < steps && rank == 0) {  // gave up: wait for the copies already on their way (a pair's, for both)
         const uint64_t t0 = now_ns();
         for (uint32_t i = k > S::kStages ? k - S::kStages : 0; i < k; ++i)
           while (!bar_try(copied(i % S::kStages), (i / S::kStages) & 1) && now_ns() - t0 < kWaitNs) {
           }
       }
     }
-  } else if (lane == 0) {
+  } else if (lane == 0 && rank == 0) {
     bool ok = true;
     for (uint32_t k = 0; k < steps; ++k) {
       const uint32_t s = k % S::kStages, parity = (k / S::kStages) & 1;
@@ -415,26 +531,30 @@ __global__ void __launch_bounds__(Tile<MT, NT, kParts>::kThreads, 1)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int p = 0; p < kParts; ++p)
-            mma(tmem + mt * NT, operand(A + mt * 16384 + kk * 2048), operand(B + p * S::kB + kk * 2048),
-                instruction<T, NT>(), k > 0 || kk > 0 || p > 0);
-      commit(empty(s));
+            mma<kPair>(tmem + mt * S::N, operand(A + mt * 16384 + kk * 2048), operand(B + p * S::kB + kk * 2048),
+                       instruction<T, S::M, S::N>(), k > 0 || kk > 0 || p > 0);
+      commit<kPair>(empty(s));
     }
     // the products issued so far end before the TMEM is freed, also when a wait ran out
-    commit(done);
+    commit<kPair>(done);
     if (!ok) {
       const uint64_t t0 = now_ns();
       while (!bar_try(done, 0) && now_ns() - t0 < kWaitNs) {
       }
-      if (a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
     }
   }
   __syncwarp();
-  __syncthreads();
+  if constexpr (kPair)
+    cluster_sync();
+  else
+    __syncthreads();
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
   if (warp == kWarps + 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kCols));
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)S::kCols));
   }
 }
 
@@ -474,21 +594,34 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-template <typename T, int MT, int NT, int kParts, bool kTma>
+template <typename T, int MT, bool kPair, int kParts, bool kTma>
 int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  using S = Tile<MT, NT, kParts>;
-  const auto kernel = k_wgrad<T, MT, NT, kParts, kTma>;
+  using S = Tile<MT, kPair, kParts>;
+  const auto kernel = k_wgrad<T, MT, kPair, kParts, kTma>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
     return HX_ERR_CUDA;
-  const dim3 grid((a.n_out + S::BM - 1) / S::BM, (a.n_in + S::BN - 1) / S::BN, a.splits);
-  kernel<<<grid, S::kThreads, S::kSmem, s>>>(map, a);
-  return launched();
+  cudaLaunchConfig_t c{};
+  const uint64_t tiles = (uint64_t)((a.n_out + S::BM - 1) / S::BM) * ((a.n_in + S::BN - 1) / S::BN);
+  if (tiles * S::kCtas >= (1ull << 31)) return HX_ERR_ARG;
+  c.gridDim = dim3((uint32_t)tiles * S::kCtas, a.splits);
+  c.blockDim = dim3(S::kThreads);
+  c.dynamicSmemBytes = S::kSmem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {S::kCtas, 1, 1};
+  c.attrs = at, c.numAttrs = kPair ? 1 : 0;
+  if (cudaLaunchKernelEx(&c, kernel, map, a) != cudaSuccess) {
+    cudaGetLastError();
+    return HX_ERR_CUDA;
+  }
+  return HX_OK;
 }
-template <typename T, int MT, int NT>
+template <typename T, int MT, bool kPair>
 int launch(bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
   if (a.fmt == HX_ROWS_E4M3)
-    return tma ? launch_tile<T, MT, NT, 1, true>(map, a, s) : launch_tile<T, MT, NT, 1, false>(map, a, s);
-  return tma ? launch_tile<T, MT, NT, 2, true>(map, a, s) : launch_tile<T, MT, NT, 2, false>(map, a, s);
+    return tma ? launch_tile<T, MT, kPair, 1, true>(map, a, s) : launch_tile<T, MT, kPair, 1, false>(map, a, s);
+  return tma ? launch_tile<T, MT, kPair, 2, true>(map, a, s) : launch_tile<T, MT, kPair, 2, false>(map, a, s);
 }
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
@@ -504,8 +637,8 @@ Plan plan(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
   Plan p{};
   constexpr uint64_t kSms = 148;
   const uint64_t steps = ceil_div(tokens, kStep);
-  p.big = ceil_div(n_out, 256) * ceil_div(n_in, 256) >= kSms;
-  const uint64_t tiles = p.big ? ceil_div(n_out, 256) * ceil_div(n_in, 256) : ceil_div(n_out, 128) * ceil_div(n_in, 128);
+  p.big = 2 * ceil_div(n_out, 512) * ceil_div(n_in, 256) >= kSms;
+  const uint64_t tiles = p.big ? 2 * ceil_div(n_out, 512) * ceil_div(n_in, 256) : ceil_div(n_out, 128) * ceil_div(n_in, 128);
   uint64_t splits = tiles < kSms ? std::min<uint64_t>(kSms / tiles, steps / 4) : 1;
   splits = std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
   // no empty splits: every one has ceil(steps / splits) steps but the last
@@ -516,7 +649,7 @@ Plan plan(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
 
 template <typename T>
 int run(const Plan& p, bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  const int rc = p.big ? launch<T, 2, 256>(tma, map, a, s) : launch<T, 1, 128>(tma, map, a, s);
+  const int rc = p.big ? launch<T, 2, true>(tma, map, a, s) : launch<T, 1, false>(tma, map, a, s);
   if (rc || a.splits == 1) return rc;
   const uint32_t grid = (uint32_t)std::min<uint64_t>(148 * 8, ceil_div((uint64_t)a.n_out * a.n_in, 256));
   if (a.dw_dtype == HX_F32)
