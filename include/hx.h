@@ -423,10 +423,12 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
  * on the tensor cores in dtype: X's values are exact there for e4m3 rows in bf16 (and in f16 within its
  * normal range), and for INT8 rows held as a sum of two (17 bits in bf16, 22 in f16); sums are in 32 bits.
  * An X beyond f16's range counts as +-65504 with HX_F16. d_workspace:
- * hx_weight_grad_workspace(tokens, n_out, n_in) bytes (0: may be NULL), 16-byte aligned, clobbered.
+ * hx_weight_grad_workspace() bytes (0: may be NULL), 16-byte aligned, clobbered; needed for rows of dY that do not
+ * start on 16 bytes, or of X on 8, which are copied first.
  * Waits inside the kernel are bounded: HX_ERR_TIMEOUT in *d_status (NULL: not reported). tokens = 0: zeros
  * (or the old values). n_out <= 2^23, n_in <= 2^22. */
-uint64_t hx_weight_grad_workspace(uint64_t tokens, uint64_t n_out, uint64_t n_in);
+uint64_t hx_weight_grad_workspace(const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes, uint64_t tokens,
+                                  uint64_t n_out, uint64_t n_in);
 int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy,
                    const uint8_t* d_bytes, const float* d_scale, uint64_t tokens, uint64_t n_out,
                    uint64_t n_in, uint32_t dw_dtype, void* d_dw, uint64_t ld_dw, int accumulate,

@@ -14,8 +14,10 @@
 // own rounding into every product: there the tile is held as two, the rounded values and the rounded
 // rest (17 bits together in bf16, 22 in f16), at twice the products. Sums are the tensor core's 32-bit accumulators.
 //
-// Few tiles: the tokens are split over several CTAs per tile, whose 32-bit partial tiles a second
-// kernel adds in order.
+// Few tiles: the tokens are split over up to 8 CTAs (4 pairs) of one cluster, which leave their 32-bit partial
+// tiles in shared memory, and each adds the others' share of its rows in their order: no workspace, no second kernel.
+//
+// Rows of dY or X that do not start on 16 bytes (TMA's rule) are first copied to rows that do.
 //
 // Every wait is bounded (2 s); when one runs out the CTA raises HX_ERR_TIMEOUT, waits for its own
 // copies in flight, frees its TMEM and returns.
@@ -34,21 +36,19 @@ using namespace hxv;
 
 constexpr int kStep = 64;             // tokens per pipeline stage
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMaxSplits = 32;
+constexpr int kMaxCluster = 8;
 constexpr int kBand = 4;              // tile rows that are walked together
 
 struct Args {
   uint32_t fmt;
-  const void* dy;  // only without TMA
-  uint64_t ld_dy;
   const uint8_t* bytes;
+  uint64_t ld_x;  // a multiple of 8, as the address
   const float* scale;
   uint64_t tokens;
   uint32_t n_out, n_in;
   void* dw;
   uint64_t ld_dw;
-  uint32_t dw_dtype, accumulate, dw_wide, x_wide;
-  float* part;         // with splits > 1: [split][n_out][n_in]
+  uint32_t dw_dtype, accumulate, dw_wide;
   uint32_t splits, steps;
   uint32_t* status;
 };
@@ -63,11 +63,13 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same on the barrier at this address in CTA `rank` of the cluster.
+// The same on the barrier at this address in CTA `rank` of the cluster. What was written before it is in the CTA's own
+// shared memory, ordered for the tensor core by fence.proxy.async; a release at cluster scope would only add a memory
+// barrier (1500 clocks per arrival, measured).
 __device__ __forceinline__ void bar_arrive_at(uint32_t bar, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar), "r"(rank)
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(bar), "r"(rank)
       : "memory");
 }
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
@@ -89,7 +91,7 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -120,37 +122,61 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 // --------------------------------------------------------------------------------- tensor core
 // Shared memory operand, MN-major with 128-byte swizzle: blocks of 64 values of M or N by 64 tokens, a
 // token's 64 values in one 128-byte line; 8 lines per swizzle atom (stride 1024), blocks 8192 apart.
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-  constexpr uint64_t kBlock = 8192 >> 4, kAtom = 1024 >> 4;
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | kBlock << 16 | kAtom << 32 | 1ull << 46 | 2ull << 61;
-}
+// Its descriptor's low word is the address / 16 beside the block stride, so that a step along the operand is an addition;
+// the high word is the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr) { return (addr & 0x3ffffu) >> 4 | (8192u >> 4) << 16; }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
 template <typename T, int M, int N>
 __device__ constexpr uint32_t instruction() {
   constexpr uint32_t type = sizeof(T) && Type<T>::kInf == 0x7f80u ? 1 : 0;  // bf16 or f16
   return 1u << 4 | type << 7 | type << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N / 8) << 17 | (uint32_t)(M / 16) << 24;
 }
-template <bool kPair>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+// kAdd: onto the accumulator. One thread issues every product, so an issue is as few instructions as it can be.
+template <bool kPair, bool kAdd>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t instr) {
   if constexpr (kPair)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kOperandHigh), "r"(instr), "n"((int)kAdd)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kOperandHigh), "r"(instr), "n"((int)kAdd)
         : "memory");
 }
-// Arrives on the barrier (of both CTAs of a pair) once the products issued so far are done.
+// The products of one stage of 64 tokens; kFirst: the tile's first.
+template <typename S, typename T, int MT, bool kPair, int kParts, bool kFirst>
+__device__ __forceinline__ void stage_products(uint32_t tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t instr = instruction<T, S::M, S::N>();
+#pragma unroll
+  for (int kk = 0; kk < kStep / 16; ++kk)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        const uint32_t x = a + ((mt * 16384 + kk * 2048) >> 4), y = b + ((p * S::kB + kk * 2048) >> 4);
+        if (kFirst && kk == 0 && p == 0)
+          mma<kPair, false>(tmem + mt * S::N, x, y, instr);
+        else
+          mma<kPair, true>(tmem + mt * S::N, x, y, instr);
+      }
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+// Arrives on the barrier (of both CTAs of a pair, the first of which has rank `first`) once the products
+// issued so far are done.
 template <bool kPair>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t first) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << first))
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -201,35 +227,6 @@ struct Barriers {
 };
 
 // ---------------------------------------------------------------------------------- conversion
-// 8 bytes of one token, columns c .. c + 7 (zeros behind the last token or column).
-__device__ __forceinline__ Bytes<8> fetch_bytes(const Args& a, uint64_t t, uint32_t c) {
-  Bytes<8> b;
-  b.b[0] = b.b[1] = 0;
-  if (t >= a.tokens || c >= a.n_in) return b;
-  const uint8_t* p = a.bytes + t * a.n_in + c;
-  if (a.x_wide) {
-    b.load(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < a.n_in) b.b[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
-  }
-  return b;
-}
-
-// 8 values of dY without TMA.
-template <typename T>
-__device__ __forceinline__ uint4 fetch_dy(const Args& a, uint64_t t, uint32_t c) {
-  uint32_t r[4] = {0, 0, 0, 0};
-  if (t < a.tokens) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.dy) + t * a.ld_dy + c;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < a.n_out) r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 template <typename T, int kParts>
 __device__ __forceinline__ void convert(uint32_t fmt, const Bytes<8>& b, float s, uint4 (&out)[kParts]) {
   float f[8];
@@ -339,7 +336,45 @@ __device__ __forceinline__ void store_block(uint32_t stage, uint32_t tm, bool an
   }
 }
 
-template <typename T, int MT, bool kPair, int kParts, bool kTma>
+// Rows y0 .. y1 - 1 of the tile at (m0, n0) from the partial tiles of the cluster's splits.
+template <typename O, uint32_t N>
+__device__ __forceinline__ void join_rows(const Args& a, uint32_t tiles, uint32_t rank, uint32_t ctas, uint32_t m0,
+                                          uint32_t n0, uint32_t y0, uint32_t y1) {
+  constexpr uint32_t kChunks = N / 4;
+  for (uint32_t i = threadIdx.x; i < (y1 - y0) * kChunks; i += blockDim.x) {
+    const uint32_t y = y0 + i / kChunks, c = i % kChunks;
+    const uint32_t row = m0 + y, col = n0 + c * 4;
+    if (row >= a.n_out || col >= a.n_in) continue;
+    const uint32_t at = tiles + y * (N * 4) + (c ^ (y & 7)) * 16;
+    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t s = 0; s < a.splits; ++s) {
+      float v[4];
+      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                   : "r"(at_rank(at, s * ctas + rank)));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] += v[k];
+    }
+    O* o = static_cast<O*>(a.dw) + (uint64_t)row * a.ld_dw + col;
+    if (a.dw_wide && col + 4 <= a.n_in) {
+      if (a.accumulate) {
+        Vec<O, 4> old;
+        old.load(o);
+        float g[4];
+        old.floats(g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] += g[k];
+      }
+      store<O, 4>(o, f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < a.n_in) o[k] = Type<O>::from_f(a.accumulate ? Type<O>::to_f(o[k]) + f[k] : f[k]);
+    }
+  }
+}
+
+template <typename T, int MT, bool kPair, int kParts>
 __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a) {
   using S = Tile<MT, kPair, kParts>;
@@ -347,16 +382,16 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bars;
   const uint32_t tiles = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_rank() : 0;
+  const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t in_cluster = cluster_rank(), split = in_cluster / S::kCtas, rank = in_cluster % S::kCtas;
+  const uint32_t first = in_cluster - rank;  // the pair's first CTA
   // Tiles in bands of kBand tile rows, columns slowest within a band: what runs at once shares 4 tiles' worth of
   // dY and about 18 of X, whose bytes are the smaller (a tile's dY takes four times its X from memory).
-  const uint32_t tile = blockIdx.x / S::kCtas, rows = (a.n_out + S::BM - 1) / S::BM, cols = (a.n_in + S::BN - 1) / S::BN;
+  const uint32_t tile = blockIdx.x / (S::kCtas * a.splits), rows = (a.n_out + S::BM - 1) / S::BM, cols = (a.n_in + S::BN - 1) / S::BN;
   const uint32_t band = tile / (kBand * cols), in_band = tile - band * kBand * cols;
   const uint32_t high = min((uint32_t)kBand, rows - band * kBand);
   const uint32_t m0 = (band * kBand + in_band % high) * S::BM + rank * 128;  // accumulator i: rows m0 + i * M ..
   const uint32_t n0 = in_band / high * S::BN, x0 = n0 + rank * 128;          // the tile's columns, the CTA's
-  const uint32_t split = blockIdx.y;
   const uint32_t per = (a.steps + a.splits - 1) / a.splits;
   const uint32_t k0 = min(split * per, a.steps), k1 = min(k0 + per, a.steps), steps = k1 - k0;
   volatile uint32_t* failed = &bars.failed;
@@ -389,12 +424,9 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  if constexpr (kPair)
-    cluster_sync();
-  else
-    __syncthreads();
+  cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&bars.tmem), 0);
 
   if (warp < kWarps) {
     // ---- converting warps. A step's chain (wait, convert, store, fence, arrive) is longer than its products
@@ -406,86 +438,89 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     const uint32_t ch = lane & 15, odd = lane >> 4;
     Bytes<8> b[kLoads];
     float sc = 0.0f;
-    const uint8_t* at = a.bytes + ((uint64_t)(k0 + group) * kStep + line0 + odd) * a.n_in + x0 + ch * 8;
+    // Loads are never conditional (a load that is chosen between is waited for on the spot): past the last token or
+    // column they go to the last one's place, and a token past the last is cleared when it is converted. Columns
+    // past the last only reach sums that are not stored.
+    const uint8_t* x = a.bytes + min((uint64_t)x0 + ch * 8, a.ld_x - 8);
     auto fetch = [&](uint32_t k) {
       const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
-      sc = 0.0f;
-      if (k < steps && t + (lane & (kTokens - 1)) < a.tokens) sc = a.scale[t + (lane & (kTokens - 1))];
-      if (a.x_wide && x0 + 128 <= a.n_in && k < steps && t + kTokens <= a.tokens) {
-        const uint8_t* p = at;
-        const uint64_t step = 2 * (uint64_t)a.n_in;
+      sc = a.scale[min(t + (lane & (kTokens - 1)), a.tokens - 1)];
+      if (t + kTokens <= a.tokens) {
+        const uint8_t* p = x + (t + odd) * a.ld_x;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j, p += step) b[j].load(p);
+        for (int j = 0; j < kLoads; ++j, p += 2 * a.ld_x) b[j].load(p);
       } else {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-          b[j] = fetch_bytes(a, k < steps ? t + 2 * j + odd : a.tokens, x0 + ch * 8);
+        for (int j = 0; j < kLoads; ++j) b[j].load(x + min(t + 2 * j + odd, a.tokens - 1) * a.ld_x);
       }
-      at += (uint64_t)kGroups * kStep * a.n_in;
     };
-    fetch(group);
+    if (group < steps) fetch(group);
     bool ok = true;
     for (uint32_t k = group; k < steps; k += kGroups) {
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
       if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)))) break;
-      const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
+      const uint32_t B = tiles + s * S::kStage + S::kA;
+      const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
+      const bool whole = t + kTokens <= a.tokens;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const uint32_t tk = 2 * j + odd, line = line0 + tk;
-        const float f = __shfl_sync(0xffffffffu, sc, tk);
+        float f = __shfl_sync(0xffffffffu, sc, tk);
+        if (!whole && t + tk >= a.tokens) b[j].b[0] = b[j].b[1] = 0, f = 0.0f;
         uint4 v[kParts];
         convert<T, kParts>(a.fmt, b[j], f, v);
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
           put(B + p * S::kB + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), v[p]);
       }
-      if constexpr (!kTma) {
-        const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
-        for (int i = 0; i < MT; ++i)
-          for (int j = 0; j < kTokens; j += 2) {
-            const uint32_t line = line0 + j + odd;
-            put(A + i * 16384 + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4),
-                fetch_dy<T>(a, t + j + odd, m0 + i * S::M + ch * 8));
-          }
-      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         if constexpr (kPair)
-          bar_arrive_at(converted(s), 0);
+          bar_arrive_at(converted(s), first);
         else
           bar_arrive(converted(s));
       }
-      fetch(k + kGroups);
+      if (k + kGroups < steps) fetch(k + kGroups);
     }
     // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
     if (ok && steps) ok = bar_wait(done, 0, failed);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (__all_sync(0xffffffffu, ok)) {
       // a block of columns at a time, the warps of a lane quarter in turn; the stages are free by now
-      const uint32_t stage = tiles + warp * 4096;
-      const bool part = a.splits > 1;
-      const uint32_t width = part || a.dw_dtype == HX_F32 ? 32 : 64;
-      for (uint32_t i = warp >> 2; i < MT * S::N / width; i += kWarps / 4) {
-        const uint32_t mt = i / (S::N / width), c = i % (S::N / width) * width;
-        const uint32_t row = m0 + mt * S::M + (warp & 3) * 32, col = n0 + c;
-        const uint32_t tm = tmem + ((warp & 3) * 32 << 16) + mt * S::N + c;
-        if (row >= a.n_out || col >= a.n_in) continue;
-        if (part)
-          store_block<float>(stage, tm, steps > 0, a.part + (uint64_t)split * a.n_out * a.n_in, a.n_in, a.n_in % 4 == 0, false,
-                             row, col, a.n_out, a.n_in);
-        else if (a.dw_dtype == HX_F32)
-          store_block<float>(stage, tm, steps > 0, static_cast<float*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col,
-                             a.n_out, a.n_in);
-        else
-          store_block<T>(stage, tm, steps > 0, static_cast<T*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col, a.n_out,
-                         a.n_in);
+      const uint32_t quarter = (warp & 3) * 32;
+      if (MT == 1 && a.splits > 1) {
+        // the partial tile: 128 rows of N sums, 16-byte chunks exchanged within eights by the row
+        for (uint32_t i = warp >> 2; i < S::N / 32; i += kWarps / 4) {
+          uint32_t r[32];
+          tmem_load32(tmem + (quarter << 16) + i * 32, r);
+          const uint32_t y = quarter + lane;
+#pragma unroll
+          for (uint32_t c = 0; c < 8; ++c)
+            put(tiles + y * (S::N * 4) + (i * 8 + (c ^ (y & 7))) * 16,
+                make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]));
+        }
+      } else {
+        const uint32_t stage = tiles + warp * 4096;
+        const uint32_t width = a.dw_dtype == HX_F32 ? 32 : 64;
+        for (uint32_t i = warp >> 2; i < MT * S::N / width; i += kWarps / 4) {
+          const uint32_t mt = i / (S::N / width), c = i % (S::N / width) * width;
+          const uint32_t row = m0 + mt * S::M + quarter, col = n0 + c;
+          const uint32_t tm = tmem + (quarter << 16) + mt * S::N + c;
+          if (row >= a.n_out || col >= a.n_in) continue;
+          if (a.dw_dtype == HX_F32)
+            store_block<float>(stage, tm, steps > 0, static_cast<float*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col,
+                               a.n_out, a.n_in);
+          else
+            store_block<T>(stage, tm, steps > 0, static_cast<T*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col, a.n_out,
+                           a.n_in);
+        }
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   } else if (warp == kWarps) {
-    if (kTma && lane == 0) {
+    if (lane == 0) {
       uint32_t k = 0;
       for (; k < steps; ++k) {
         const uint32_t s = k % S::kStages;
@@ -494,7 +529,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
         if constexpr (kPair) {
           // both CTAs' copies count on the first one's barrier
           if (rank == 0) bar_expect(copied(s), 2 * S::kA);
-          const uint32_t bar = at_rank(copied(s), 0);
+          const uint32_t bar = at_rank(copied(s), first);
           for (int i = 0; i < 2 * MT; ++i)
             asm volatile(
                 "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -518,36 +553,46 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
           }
       }
     }
-  } else if (lane == 0 && rank == 0) {
+  } else if (rank == 0) {
+    // the whole warp walks the steps, so that what the products take stays in uniform registers; one lane issues
     bool ok = true;
+    const uint32_t a0 = operand(tiles), b0 = operand(tiles + S::kA);
+    uint32_t s = 0, parity = 0;
     for (uint32_t k = 0; k < steps; ++k) {
-      const uint32_t s = k % S::kStages, parity = (k / S::kStages) & 1;
-      if (!(ok = bar_wait(converted(s), parity, failed) && (!kTma || bar_wait(copied(s), parity, failed)))) break;
+      ok = bar_wait(converted(s), parity, failed) && bar_wait(copied(s), parity, failed);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t A = tiles + s * S::kStage, B = A + S::kA;
-#pragma unroll
-      for (int kk = 0; kk < kStep / 16; ++kk)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int p = 0; p < kParts; ++p)
-            mma<kPair>(tmem + mt * S::N, operand(A + mt * 16384 + kk * 2048), operand(B + p * S::kB + kk * 2048),
-                       instruction<T, S::M, S::N>(), k > 0 || kk > 0 || p > 0);
-      commit<kPair>(empty(s));
+      const uint32_t at = s * (S::kStage >> 4);
+      if (elected()) {
+        if (k == 0)
+          stage_products<S, T, MT, kPair, kParts, true>(tmem, a0 + at, b0 + at);
+        else
+          stage_products<S, T, MT, kPair, kParts, false>(tmem, a0 + at, b0 + at);
+        commit<kPair>(empty(s), first);
+      }
+      __syncwarp();
+      if (++s == S::kStages) s = 0, parity ^= 1;
     }
     // the products issued so far end before the TMEM is freed, also when a wait ran out
-    commit<kPair>(done);
-    if (!ok) {
+    if (elected()) commit<kPair>(done, first);
+    if (!ok && lane == 0) {
       const uint64_t t0 = now_ns();
       while (!bar_try(done, 0) && now_ns() - t0 < kWaitNs) {
       }
     }
   }
   __syncwarp();
-  if constexpr (kPair)
-    cluster_sync();
-  else
-    __syncthreads();
+  cluster_sync();
+  if (MT == 1 && a.splits > 1) {
+    // this split's share of the rows: the splits' sums in their order, four columns per thread
+    const uint32_t y0 = split * 128 / a.splits, y1 = (split + 1) * 128 / a.splits;
+    if (a.dw_dtype == HX_F32)
+      join_rows<float, S::N>(a, tiles, rank, S::kCtas, m0, n0, y0, y1);
+    else
+      join_rows<T, S::N>(a, tiles, rank, S::kCtas, m0, n0, y0, y1);
+    __syncwarp();
+    cluster_sync();  // a CTA's sums stay until every other one has read them
+  }
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
   if (warp == kWarps + 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -558,18 +603,30 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
   }
 }
 
-// dW = (old dW if accumulate) + the splits' partial sums, in their order.
-template <typename O>
+// Copies rows to a pitch that TMA and the 8-byte loads take: `chunks` pieces of 8 bytes per row, the last
+// one zero-filled. E: the element (2 or 1 bytes).
+template <typename E>
+__device__ __forceinline__ void align_piece(const E* src, uint64_t ld, uint64_t cols, uint64_t* dst, uint32_t chunks, uint64_t i) {
+  constexpr uint32_t kPer = 8 / sizeof(E);
+  const uint64_t row = i / chunks, c = (i - row * chunks) * kPer;
+  const E* p = src + row * ld + c;
+  uint64_t v = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kPer; ++k)
+    if (c + k < cols) v |= (uint64_t)p[k] << (8 * sizeof(E) * k);
+  dst[i] = v;
+}
 __global__ void __launch_bounds__(256)
-    k_wgrad_join(const float* __restrict__ part, uint32_t splits, uint32_t n_out, uint32_t n_in, O* dw,
-                 uint64_t ld, uint32_t accumulate) {
-  const uint64_t all = (uint64_t)n_out * n_in;
-  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
-    const uint64_t row = i >> 32 ? i / n_in : (uint32_t)i / n_in;
-    O* o = dw + row * ld + (i - row * n_in);
-    float v = accumulate ? Type<O>::to_f(*o) : 0.0f, sum = 0.0f;
-    for (uint32_t s = 0; s < splits; ++s) sum += part[s * all + i];
-    *o = Type<O>::from_f(v + sum);
+    k_wgrad_align(const uint16_t* dy, uint64_t ld_dy, uint64_t n_out, uint64_t* dy_out, const uint8_t* x, uint64_t n_in,
+                  uint64_t* x_out, uint64_t tokens, uint32_t dy_blocks) {
+  const uint32_t cy = (uint32_t)((n_out + 7) / 8 * 2), cx = (uint32_t)((n_in + 15) / 16 * 2);
+  const bool first = blockIdx.x < dy_blocks;
+  const uint64_t all = tokens * (first ? cy : cx), step = (uint64_t)(first ? dy_blocks : gridDim.x - dy_blocks) * 256;
+  for (uint64_t i = (uint64_t)(first ? blockIdx.x : blockIdx.x - dy_blocks) * 256 + threadIdx.x; i < all; i += step) {
+    if (first)
+      align_piece<uint16_t>(dy, ld_dy, n_out, dy_out, cy, i);
+    else
+      align_piece<uint8_t>(x, n_in, n_in, x_out, cx, i);
   }
 }
 
@@ -594,23 +651,25 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-template <typename T, int MT, bool kPair, int kParts, bool kTma>
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+template <typename T, int MT, bool kPair, int kParts>
 int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
   using S = Tile<MT, kPair, kParts>;
-  const auto kernel = k_wgrad<T, MT, kPair, kParts, kTma>;
+  const auto kernel = k_wgrad<T, MT, kPair, kParts>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
     return HX_ERR_CUDA;
+  const uint64_t ctas = ceil_div(a.n_out, S::BM) * ceil_div(a.n_in, S::BN) * S::kCtas * a.splits;
+  if (ctas >= (1ull << 31)) return HX_ERR_ARG;
   cudaLaunchConfig_t c{};
-  const uint64_t tiles = (uint64_t)((a.n_out + S::BM - 1) / S::BM) * ((a.n_in + S::BN - 1) / S::BN);
-  if (tiles * S::kCtas >= (1ull << 31)) return HX_ERR_ARG;
-  c.gridDim = dim3((uint32_t)tiles * S::kCtas, a.splits);
+  c.gridDim = dim3((uint32_t)ctas);
   c.blockDim = dim3(S::kThreads);
   c.dynamicSmemBytes = S::kSmem;
   c.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {S::kCtas, 1, 1};
-  c.attrs = at, c.numAttrs = kPair ? 1 : 0;
+  at[0].val.clusterDim = {S::kCtas * a.splits, 1, 1};
+  c.attrs = at, c.numAttrs = 1;
   if (cudaLaunchKernelEx(&c, kernel, map, a) != cudaSuccess) {
     cudaGetLastError();
     return HX_ERR_CUDA;
@@ -618,59 +677,74 @@ int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
   return HX_OK;
 }
 template <typename T, int MT, bool kPair>
-int launch(bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  if (a.fmt == HX_ROWS_E4M3)
-    return tma ? launch_tile<T, MT, kPair, 1, true>(map, a, s) : launch_tile<T, MT, kPair, 1, false>(map, a, s);
-  return tma ? launch_tile<T, MT, kPair, 2, true>(map, a, s) : launch_tile<T, MT, kPair, 2, false>(map, a, s);
+int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  return a.fmt == HX_ROWS_E4M3 ? launch_tile<T, MT, kPair, 1>(map, a, s) : launch_tile<T, MT, kPair, 2>(map, a, s);
 }
 
-uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
-
+// The tile and the number of splits of the tokens, by the estimated time: rounds of CTAs over 148 SMs, each
+// round its steps and a fixed part (start, first loads, last products, stores). Clocks per step of 64 tokens as
+// measured: PLAN_COMMENT
 struct Plan {
-  bool big;
+  int mt;
+  bool pair;
   uint32_t splits;
 };
-
-// Tiles of 256 x 256 once they fill the GPU (148 SMs), else of 128 x 128; tokens split so that the
-// CTAs fill it once, at least 4 steps of 64 tokens each.
-Plan plan(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
-  Plan p{};
+Plan plan(uint32_t fmt, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
   constexpr uint64_t kSms = 148;
+  struct Kind {
+    int mt;
+    bool pair;
+    uint64_t rows, cols, step[2], fixed;
+  };
+  static constexpr Kind kinds[3] = {{1, false, 128, 128, {700, 1100}, 9000},
+                                    {1, true, 256, 256, {850, 1400}, 10000},
+                                    {2, true, 512, 256, {1300, 2300}, 14000}};
   const uint64_t steps = ceil_div(tokens, kStep);
-  p.big = 2 * ceil_div(n_out, 512) * ceil_div(n_in, 256) >= kSms;
-  const uint64_t tiles = p.big ? 2 * ceil_div(n_out, 512) * ceil_div(n_in, 256) : ceil_div(n_out, 128) * ceil_div(n_in, 128);
-  uint64_t splits = tiles < kSms ? std::min<uint64_t>(kSms / tiles, steps / 4) : 1;
-  splits = std::max<uint64_t>(1, std::min<uint64_t>(splits, kMaxSplits));
-  // no empty splits: every one has ceil(steps / splits) steps but the last
-  if (steps) splits = ceil_div(steps, ceil_div(steps, splits));
-  p.splits = (uint32_t)splits;
-  return p;
+  Plan best{1, false, 1};
+  uint64_t least = ~0ull;
+  for (const Kind& k : kinds) {
+    const uint64_t ctas = ceil_div(n_out, k.rows) * ceil_div(n_in, k.cols) * (k.pair ? 2 : 1);
+    const uint64_t most = k.mt == 2 ? 1 : kMaxCluster / (k.pair ? 2 : 1);
+    for (uint64_t s = 1; s <= most && s <= std::max<uint64_t>(1, steps); ++s) {
+      const uint64_t per = ceil_div(steps, s);
+      if (s > 1 && ceil_div(steps, per) != s) continue;  // an empty split
+      const uint64_t t = ceil_div(ctas * s, kSms) * (per * k.step[fmt == HX_ROWS_INT8] + k.fixed + (s > 1 ? 2000 : 0));
+      if (t < least) least = t, best = Plan{k.mt, k.pair, (uint32_t)s};
+    }
+  }
+  return best;
 }
 
 template <typename T>
-int run(const Plan& p, bool tma, const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  const int rc = p.big ? launch<T, 2, true>(tma, map, a, s) : launch<T, 1, false>(tma, map, a, s);
-  if (rc || a.splits == 1) return rc;
-  const uint32_t grid = (uint32_t)std::min<uint64_t>(148 * 8, ceil_div((uint64_t)a.n_out * a.n_in, 256));
-  if (a.dw_dtype == HX_F32)
-    k_wgrad_join<float><<<grid, 256, 0, s>>>(a.part, a.splits, a.n_out, a.n_in, static_cast<float*>(a.dw), a.ld_dw, a.accumulate);
-  else
-    k_wgrad_join<T><<<grid, 256, 0, s>>>(a.part, a.splits, a.n_out, a.n_in, static_cast<T*>(a.dw), a.ld_dw, a.accumulate);
-  return launched();
+int run(const Plan& p, const CUtensorMap& map, const Args& a, cudaStream_t s) {
+  if (p.mt == 2) return launch<T, 2, true>(map, a, s);
+  return p.pair ? launch<T, 1, true>(map, a, s) : launch<T, 1, false>(map, a, s);
 }
 
 bool bad_sizes(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
   return tokens >= (1ull << 31) - 64 || !n_out || !n_in || n_out > (1ull << 23) || n_in > (1ull << 22);
 }
 
+// What is copied to aligned rows first, and where: bytes of the workspace for dY, then for X.
+struct Copies {
+  uint64_t dy, x;
+};
+Copies copies(const void* dy, uint64_t ld_dy, const void* bytes, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+  Copies c{};
+  if (!multiple(dy, 16) || (tokens > 1 && ld_dy % 8)) c.dy = tokens * ((n_out + 7) / 8 * 16);
+  if (!multiple(bytes, 8) || n_in % 8) c.x = tokens * ((n_in + 15) / 16 * 16);
+  return c;
+}
+
 }  // namespace
 
 extern "C" {
 
-uint64_t hx_weight_grad_workspace(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+uint64_t hx_weight_grad_workspace(const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes, uint64_t tokens,
+                                  uint64_t n_out, uint64_t n_in) {
   if (bad_sizes(tokens, n_out, n_in)) return 0;
-  const Plan p = plan(tokens, n_out, n_in);
-  return p.splits > 1 ? p.splits * n_out * n_in * 4 : 0;
+  const Copies c = copies(d_dy, ld_dy, d_bytes, tokens, n_out, n_in);
+  return c.dy + c.x;
 }
 
 int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes,
@@ -682,36 +756,44 @@ int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t l
   if (bad_sizes(tokens, n_out, n_in) || (tokens > 1 && ld_dy < n_out) || (n_out > 1 && ld_dw < n_in)) return HX_ERR_ARG;
   if (!d_dw || !multiple(d_dw, dw_dtype == HX_F32 ? 4 : 2) || !multiple(d_status, 4)) return HX_ERR_ARG;
   if (tokens && (!d_dy || !d_bytes || !d_scale || !multiple(d_dy, 2) || !multiple(d_scale, 4))) return HX_ERR_ARG;
+  if (tokens > 1 && ld_dy >= (1ull << 39)) return HX_ERR_ARG;  // TMA's largest stride
   if (!tokens && accumulate) return HX_OK;
-  const Plan p = plan(tokens, n_out, n_in);
-  if (p.splits > 1 && (!d_workspace || !multiple(d_workspace, 16) ||
-                       workspace_bytes < hx_weight_grad_workspace(tokens, n_out, n_in)))
+  const Copies need = copies(d_dy, ld_dy, d_bytes, tokens, n_out, n_in);
+  if (need.dy + need.x && (!d_workspace || !multiple(d_workspace, 16) || workspace_bytes < need.dy + need.x))
     return HX_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Plan p = plan(format, tokens, n_out, n_in);
   Args a{};
-  a.fmt = format, a.dy = d_dy, a.ld_dy = ld_dy, a.bytes = d_bytes, a.scale = d_scale;
+  a.fmt = format, a.bytes = d_bytes, a.ld_x = n_in, a.scale = d_scale;
   a.tokens = tokens, a.n_out = (uint32_t)n_out, a.n_in = (uint32_t)n_in;
   a.dw = d_dw, a.ld_dw = ld_dw, a.dw_dtype = dw_dtype, a.accumulate = accumulate != 0;
   a.dw_wide = multiple(d_dw, 16) && (n_out == 1 || ld_dw * (dw_dtype == HX_F32 ? 4 : 2) % 16 == 0);
-  a.x_wide = n_in % 8 == 0 && multiple(d_bytes, 8);
-  a.part = static_cast<float*>(d_workspace), a.splits = p.splits;
-  a.steps = (uint32_t)ceil_div(tokens, kStep), a.status = d_status;
-  // TMA wants rows that start on 16 bytes
-  const uint64_t pitch = tokens > 1 ? ld_dy * 2 : (n_out * 2 + 15) / 16 * 16;
-  const bool tma = tokens && multiple(d_dy, 16) && pitch % 16 == 0 && pitch < (1ull << 40);
+  a.splits = p.splits, a.steps = (uint32_t)ceil_div(tokens, kStep), a.status = d_status;
+  const void* dy = d_dy;
+  uint64_t pitch = tokens > 1 ? ld_dy * 2 : (n_out + 7) / 8 * 16;
+  if (need.dy + need.x) {
+    uint8_t* w = static_cast<uint8_t*>(d_workspace);
+    const uint64_t by = ceil_div(need.dy / 8, 256), bx = ceil_div(need.x / 8, 256), most = 148 * 16;
+    const uint32_t gy = (uint32_t)std::min(by, most), gx = (uint32_t)std::min(bx, most);
+    k_wgrad_align<<<gy + gx, 256, 0, s>>>(static_cast<const uint16_t*>(d_dy), ld_dy, n_out, reinterpret_cast<uint64_t*>(w),
+                                          d_bytes, n_in, reinterpret_cast<uint64_t*>(w + need.dy), tokens, gy);
+    if (const int rc = launched()) return rc;
+    if (need.dy) dy = w, pitch = (n_out + 7) / 8 * 16;
+    if (need.x) a.bytes = w + need.dy, a.ld_x = (n_in + 15) / 16 * 16;
+  }
   CUtensorMap map{};
-  if (tma) {
+  if (tokens) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return HX_ERR_CUDA;
     const cuuint64_t dims[2] = {n_out, tokens}, strides[1] = {pitch};
     const cuuint32_t box[2] = {64, kStep}, unit[2] = {1, 1};
     if (fn(&map, dtype == HX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-           const_cast<void*>(d_dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           const_cast<void*>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return HX_ERR_CUDA;
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == HX_F16 ? run<__half>(p, tma, map, a, s) : run<__nv_bfloat16>(p, tma, map, a, s);
+  return dtype == HX_F16 ? run<__half>(p, map, a, s) : run<__nv_bfloat16>(p, map, a, s);
 }
 
 }  // extern "C"

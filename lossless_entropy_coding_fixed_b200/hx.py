@@ -107,7 +107,7 @@ def lib():
             "hx_head_norm_rope_workspace": (u64, [u32]),
             "hx_head_norm_rope_backward": (i32, [P, P, u64, u64, P, P, P, u64,
                                                  u64, P, P, P, u64, P, P]),
-            "hx_weight_grad_workspace": (u64, [u64, u64, u64]),
+            "hx_weight_grad_workspace": (u64, [P, u64, P, u64, u64, u64]),
             "hx_weight_grad": (i32, [u32, u32, P, u64, P, P, u64, u64, u64, u32, P, u64, i32, P, u64, P, P]),
             "hx_entropy": (ctypes.c_double, [P]),
             "hx_mean_length": (ctypes.c_double, [P, CB]),
@@ -799,8 +799,9 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
         _same(out, "out", (n_out, n_in), dtype or out.dtype, dev)
     ldw = _matrix(out, "out")[2]
     fn = lib()
-    need = fn.hx_weight_grad_workspace(tokens, n_out, n_in)
+    yp = dy.data_ptr()
+    need = fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
     ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
-    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, dy.data_ptr(), ld, db, sp, tokens, n_out, n_in, _dtype(out),
+    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, _dtype(out),
             out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
     return out

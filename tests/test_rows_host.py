@@ -158,14 +158,16 @@ def test_weight_grad_refusals():
                dict(ld=63), dict(ldw=31), dict(n=0), dict(k=0), dict(t=1 << 31), dict(n=(1 << 23) + 1, ld=1 << 24),
                dict(k=(1 << 22) + 1, ldw=1 << 23), dict(dy=A + 1), dict(dw=A + 1), dict(s=A + 2), dict(st=A + 2)):
         assert call(**kw) == bad, kw
-    need = L.hx_weight_grad_workspace(4096, 64, 32)
-    assert need > 0 and need % (4 * 64 * 32) == 0
-    assert call(t=4096, ws=None) == bad
-    assert call(t=4096, wsb=need - 1) == bad
-    assert call(t=4096, ws=A + 4) == bad
+    need = L.hx_weight_grad_workspace
+    assert need(A, 64, A, 128, 64, 32) == 0  # rows that TMA takes as they are
+    odd = need(A, 65, A, 128, 64, 32)
+    assert odd >= 128 * 64 * 2 and need(A + 2, 64, A, 128, 64, 32) == odd
+    assert need(A, 64, A + 1, 128, 64, 32) >= 128 * 32 and need(A, 64, A, 128, 64, 33) >= 128 * 33
+    assert call(ld=65, ws=None) == bad
+    assert call(ld=65, wsb=odd - 1) == bad
+    assert call(ld=65, ws=A + 4) == bad
     assert call(t=0, acc=1, dy=None, b=None, s=None) == 0  # nothing to add
-    assert L.hx_weight_grad_workspace(4096, 8192, 8192) == 0  # enough tiles: the tokens are not split
-    assert L.hx_weight_grad_workspace(0, 64, 32) == 0
+    assert need(None, 64, None, 0, 64, 32) == 0
 
 
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
