@@ -227,10 +227,11 @@ struct Barriers {
 };
 
 // ---------------------------------------------------------------------------------- conversion
+// 8 bytes of a row with scale s as values of type T, in kParts parts (1: e4m3, 2: INT8).
 template <typename T, int kParts>
-__device__ __forceinline__ void convert(uint32_t fmt, const Bytes<8>& b, float s, uint4 (&out)[kParts]) {
+__device__ __forceinline__ void convert(const Bytes<8>& b, float s, uint4 (&out)[kParts]) {
   float f[8];
-  to_values<8>(fmt, b, s, f);
+  to_values<8>(kParts == 1 ? HX_ROWS_E4M3 : HX_ROWS_INT8, b, s, f);
   if constexpr (Type<T>::kInf == 0x7c00u) {
     // a row near fp16's largest value can round above it in its byte
 #pragma unroll
@@ -249,6 +250,24 @@ __device__ __forceinline__ void convert(uint32_t fmt, const Bytes<8>& b, float s
     }
     out[p] = make_uint4(r[0], r[1], r[2], r[3]);
   }
+}
+
+// The same for e4m3 in bf16 and a scale that bf16 holds (twice in s2; every scale of the library's): e4m3's values are
+// exact in bf16, so one packed product there rounds as the 32-bit product would.
+__device__ __forceinline__ uint4 convert_bf16(const Bytes<8>& b, uint32_t s2) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h0, h1;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(b.b[i]));
+    const float2 v0 = unpack2<__half>(h0), v1 = unpack2<__half>(h1);
+    const uint32_t w0 = pack2<__nv_bfloat16>(v0.x, v0.y), w1 = pack2<__nv_bfloat16>(v1.x, v1.y);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(w0), "r"(s2));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i + 1]) : "r"(w1), "r"(s2));
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 __device__ __forceinline__ void put(uint32_t addr, const uint4& v) {
@@ -460,19 +479,30 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
       if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)))) break;
-      const uint32_t B = tiles + s * S::kStage + S::kA;
+      // line line0 + 2 j + odd, its chunks exchanged by the line's place in its eight
+      const uint32_t B = tiles + s * S::kStage + S::kA + (ch >> 3) * 8192 + (line0 + odd) * 128;
+      const uint32_t swap = ((ch ^ odd) & 7) << 4;
       const uint64_t t = (uint64_t)(k0 + k) * kStep + line0;
-      const bool whole = t + kTokens <= a.tokens;
+      if (t + kTokens > a.tokens) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const uint32_t tk = 2 * j + odd, line = line0 + tk;
-        float f = __shfl_sync(0xffffffffu, sc, tk);
-        if (!whole && t + tk >= a.tokens) b[j].b[0] = b[j].b[1] = 0, f = 0.0f;
-        uint4 v[kParts];
-        convert<T, kParts>(a.fmt, b[j], f, v);
+        for (int j = 0; j < kLoads; ++j)
+          if (t + 2 * j + odd >= a.tokens) b[j].b[0] = b[j].b[1] = 0;
+        if (t + (lane & (kTokens - 1)) >= a.tokens) sc = 0.0f;
+      }
+      const uint32_t bits = __float_as_uint(sc);
+      if (kParts == 1 && Type<T>::kInf == 0x7f80u && __all_sync(0xffffffffu, (bits & 0xffffu) == 0)) {
+        const uint32_t s2 = bits | bits >> 16;
 #pragma unroll
-        for (int p = 0; p < kParts; ++p)
-          put(B + p * S::kB + (ch >> 3) * 8192 + line * 128 + (((ch ^ line) & 7) << 4), v[p]);
+        for (int j = 0; j < kLoads; ++j)
+          put(B + j * 256 + (swap ^ ((2 * j & 7) << 4)), convert_bf16(b[j], __shfl_sync(0xffffffffu, s2, 2 * j + odd)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          uint4 v[kParts];
+          convert<T, kParts>(b[j], __shfl_sync(0xffffffffu, sc, 2 * j + odd), v);
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) put(B + p * S::kB + j * 256 + (swap ^ ((2 * j & 7) << 4)), v[p]);
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
