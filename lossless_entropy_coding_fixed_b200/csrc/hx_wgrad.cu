@@ -711,24 +711,31 @@ int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
   return a.fmt == HX_ROWS_E4M3 ? launch_tile<T, MT, kPair, 1>(map, a, s) : launch_tile<T, MT, kPair, 2>(map, a, s);
 }
 
-// The tile and the number of splits of the tokens, by the estimated time: rounds of CTAs over 148 SMs, each
-// round its steps and a fixed part (start, first loads, last products, stores). Clocks per step of 64 tokens as
-// measured: PLAN_COMMENT
+// The tile and the number of splits of the tokens, by the estimated time: rounds of CTAs over the SMs, each
+// its steps of 64 tokens and a fixed part (start, first loads, last products, stores), in nanoseconds as measured on
+// B200 (e4m3, INT8). A 128 x 128 tile's step is bound by shared memory (64 KB in and out, 512 clocks for 256 of
+// products), a pair's 256 x 256 as much for twice the products per CTA, a pair's 512 x 256 by the products. So: large
+// tiles where they fill the GPU, else small ones with more splits. Measured (us), e4m3, tokens x out x in:
+//   4096 x 256 x 256    one tile each: 26.6 / 27.7 / 42.4;  128 x 128 in 8 splits 10.6
+//   4096 x 1024 x 1024  27.3 / 28.4 / 44.1;  256 x 256 in 3 splits 18.0, 128 x 128 in 2 18.8
+//   8192 x 2048 x 2048  95.8 / 51.2 / 79.9
+//   4096 x 4096 x 4096  183 / 114 / 94
 struct Plan {
   int mt;
   bool pair;
   uint32_t splits;
 };
 Plan plan(uint32_t fmt, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
-  constexpr uint64_t kSms = 148;
   struct Kind {
     int mt;
     bool pair;
-    uint64_t rows, cols, step[2], fixed;
+    uint64_t rows, cols, step[2], fixed, join;
   };
-  static constexpr Kind kinds[3] = {{1, false, 128, 128, {700, 1100}, 9000},
-                                    {1, true, 256, 256, {850, 1400}, 10000},
-                                    {2, true, 512, 256, {1300, 2300}, 14000}};
+  static constexpr Kind kinds[3] = {{1, false, 128, 128, {325, 490}, 5000, 2200},
+                                    {1, true, 256, 256, {320, 555}, 6000, 3600},
+                                    {2, true, 512, 256, {555, 1110}, 8000, 0}};
+  // SMs that clusters of 1 .. 8 CTAs, one per SM, can have at once (the runtime's count of clusters on a B200)
+  static constexpr uint64_t kSms[kMaxCluster + 1] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
   const uint64_t steps = ceil_div(tokens, kStep);
   Plan best{1, false, 1};
   uint64_t least = ~0ull;
@@ -738,7 +745,7 @@ Plan plan(uint32_t fmt, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
     for (uint64_t s = 1; s <= most && s <= std::max<uint64_t>(1, steps); ++s) {
       const uint64_t per = ceil_div(steps, s);
       if (s > 1 && ceil_div(steps, per) != s) continue;  // an empty split
-      const uint64_t t = ceil_div(ctas * s, kSms) * (per * k.step[fmt == HX_ROWS_INT8] + k.fixed + (s > 1 ? 2000 : 0));
+      const uint64_t t = ceil_div(ctas * s, kSms[s * (k.pair ? 2 : 1)]) * (per * k.step[fmt == HX_ROWS_INT8] + k.fixed + (s > 1 ? k.join : 0));
       if (t < least) least = t, best = Plan{k.mt, k.pair, (uint32_t)s};
     }
   }

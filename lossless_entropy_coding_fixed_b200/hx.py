@@ -597,7 +597,7 @@ def quantize_rows(x, fmt: int = ROWS_E4M3, out=None, scale=None):
     dt = _dtype(x)
     rows, cols, ld = _matrix(x, "x")
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        out = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
         ob = out.data_ptr()
     else:
         ob = _dense(out, "out", (rows, cols), torch.uint8, dev)
@@ -639,14 +639,14 @@ def gated_forward(x, fmt: int = ROWS_E4M3, save: bool = True, out=None):
     if both % 2:
         raise ValueError("x must have as many gate columns as up columns")
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        out = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
         op = out.data_ptr()
     else:
         op = _dense(out, "out", (rows, cols), x.dtype, dev)
     data = scale = db = sp = None
     if save:
-        data = torch.empty((rows, 2, cols), dtype=torch.uint8, device=x.device)
-        scale = torch.empty((rows, 2), dtype=torch.float32, device=x.device)
+        data = torch.empty(rows, 2, cols, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(rows, 2, dtype=torch.float32, device=x.device)
         db, sp = data.data_ptr(), scale.data_ptr()
     _launch(dev, "hx_gated_forward", lib().hx_gated_forward, fmt, dt, x.data_ptr(), rows, cols, ld, op, db, sp)
     return out, data, scale
@@ -661,8 +661,8 @@ def gated_backward(dh, data, scale, fmt: int = ROWS_E4M3, need_h: bool = False):
     rows, cols, ld = _matrix(dh, "dh")
     db = _dense(data, "bytes", (rows, 2, cols), torch.uint8, dev)
     sp = _dense(scale, "scale", (rows, 2), torch.float32, dev)
-    dx = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dh.device)
-    h = torch.empty((rows, cols), dtype=dh.dtype, device=dh.device) if need_h else None
+    dx = torch.empty(rows, 2 * cols, dtype=dh.dtype, device=dh.device)
+    h = torch.empty(rows, cols, dtype=dh.dtype, device=dh.device) if need_h else None
     _launch(dev, "hx_gated_backward", lib().hx_gated_backward, fmt, dt, dh.data_ptr(), ld, db, sp, rows, cols,
             dx.data_ptr(), h.data_ptr() if need_h else None)
     return dx, h
@@ -794,7 +794,7 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((n_out, n_in), dtype=dtype or dy.dtype, device=dy.device)
+        out = torch.empty(n_out, n_in, dtype=dtype or dy.dtype, device=dy.device)
     else:
         _same(out, "out", (n_out, n_in), dtype or out.dtype, dev)
     ldw = _matrix(out, "out")[2]
