@@ -64,7 +64,7 @@ struct Units {
   }
 };
 
-// A lane's 16 values as 8 slots of two, for the packed 32-bit arithmetic. Vectors of 2 or more: slots
+// A lane's 16 values as 8 slots of two. Vectors of 2 or more: slots
 // are neighbours, first those of vector 0, then those of vector 1; vectors of 1: slot j is unit j's (a, b).
 // The other value of a pair is in the same slot (kSwap) or in the same place of the other vector.
 template <int PU, bool kInter>
@@ -76,22 +76,12 @@ struct Slots {
   static constexpr __device__ bool second(int k) { return !kSwap && k % PU >= H; }
 };
 
-__device__ __forceinline__ uint64_t as_u64(float2 v) {
-  return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
-}
-__device__ __forceinline__ float2 as_f2(uint64_t v) {
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
+// (Two scalar operations: the packed ones cost more in moves to register pairs than they save, 53 -> 49 us forward and
+// 65 -> 60 backward at 8192 tokens of 40 heads of 128.)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
-  return as_f2(d);
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
-  return as_f2(d);
-}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
 
@@ -207,7 +197,7 @@ __device__ __forceinline__ void split_item(uint64_t i, uint32_t chunks, uint64_t
 
 // With the weight folded into the turn, y = r (x * (w c) + other(x) * (other(w) s)): the products
 // w c and w s are made once per token and group of heads.
-template <typename T, int PU, bool kInter>
+template <typename T, int PU, bool kInter, uint32_t kFmt>
 __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constant__ Args a) {
   using S = Slots<PU, kInter>;
   const Units<PU, kInter> un(a);
@@ -274,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
     if (!ok) r = __uint_as_float(0x7fc00000u);
     if (a.bytes) {
       top = group_max(top_bits<T>(top), a.lanes);
-      const Scale sc = scale_of<T>(a.fmt, top);
+      const Scale sc = scale_of<T>(kFmt, top);
       if (h < h1) {
         if (sub == 0) a.scale[row] = sc.s;
         uint8_t* b = a.bytes + row * a.dim;
@@ -284,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
           if (!un.has(u)) continue;
           float f0[PU], f1[PU];
           from_slots<PU>(j, v, f0, f1);
-          to_bytes<PU>(a.fmt, f0, sc).store(b + un.off0(u));
-          to_bytes<PU>(a.fmt, f1, sc).store(b + un.off1(u));
+          to_bytes<PU>(kFmt, f0, sc).store(b + un.off0(u));
+          to_bytes<PU>(kFmt, f1, sc).store(b + un.off1(u));
         }
       }
     }
@@ -310,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
 }
 
 // In terms of the bytes' values q (x~ = s q): n = q s r, dw += g n, dx = r (g w - n mean(g w n)).
-template <typename T, int PU, bool kInter>
+template <typename T, int PU, bool kInter, uint32_t kFmt>
 __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_constant__ Args a) {
   using S = Slots<PU, kInter>;
   __shared__ float sums[kThreads * 16];
@@ -380,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
         v0[j].floats(f0);
         v1[j].floats(f1);
         to_slots<PU>(j, f0, f1, g);
-        to_values<PU>(a.fmt, b0[j], 1.0f, f0);
-        to_values<PU>(a.fmt, b1[j], 1.0f, f1);
+        to_values<PU>(kFmt, b0[j], 1.0f, f0);
+        to_values<PU>(kFmt, b1[j], 1.0f, f1);
         to_slots<PU>(j, f0, f1, q);
       }
       fetch(h + 1 < h1);
@@ -447,26 +437,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
   }
 }
 
-// Sums the blocks' partial weight gradients in a fixed order: 8 interleaved sums per column, then
-// those 8. blockIdx.y: 0 queries, 1 keys.
-__global__ void __launch_bounds__(256) k_qk_weights(const float* __restrict__ part, uint32_t dim,
-                                                    uint32_t blocks_q, uint32_t blocks,
-                                                    float* dwq, float* dwk) {
-  __shared__ float rows[8][32];
-  const uint32_t d = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+// Sums the blocks' partial weight gradients in a fixed order: 32 interleaved sums per column, then
+// those 32. blockIdx.y: 0 queries, 1 keys.
+__global__ void __launch_bounds__(1024) k_qk_weights(const float* __restrict__ part, uint32_t dim,
+                                                     uint32_t blocks_q, uint32_t blocks,
+                                                     float* dwq, float* dwk) {
+  __shared__ float rows[32][33];
+  const uint32_t x = threadIdx.x & 31, k = threadIdx.x >> 5, d = blockIdx.x * 32 + x;
   const uint32_t lo = blockIdx.y ? blocks_q : 0, hi = blockIdx.y ? blocks : blocks_q;
   float* dw = blockIdx.y ? dwk : dwq;
   float v = 0.0f;
-  if (d < dim)
-    for (uint32_t b = lo + k; b < hi; b += 8) v += part[(uint64_t)b * dim + d];
-  rows[k][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (k == 0 && d < dim && dw) {
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += rows[i][threadIdx.x];
-    dw[d] = v;
+  if (d < dim) {
+#pragma unroll 8
+    for (uint32_t b = lo + k; b < hi; b += 32) v += part[(uint64_t)b * dim + d];
   }
+  rows[k][x] = v;
+  __syncthreads();
+  v = rows[x][k];  // column k of the block's 32, slice x
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (x == 0 && blockIdx.x * 32 + k < dim && dw) dw[blockIdx.x * 32 + k] = v;
 }
 
 // ------------------------------------------------------------------------------------- launch
@@ -497,10 +487,14 @@ int vector_of(const Args& a, uint64_t e) {
 
 template <typename T, int PU, bool kInter>
 int launch(bool backward, const Args& a, uint32_t grid, cudaStream_t s) {
-  if (backward)
-    k_qk_backward<T, PU, kInter><<<grid, kThreads, 0, s>>>(a);
+  if (backward && a.fmt == HX_ROWS_E4M3)
+    k_qk_backward<T, PU, kInter, HX_ROWS_E4M3><<<grid, kThreads, 0, s>>>(a);
+  else if (backward)
+    k_qk_backward<T, PU, kInter, HX_ROWS_INT8><<<grid, kThreads, 0, s>>>(a);
+  else if (a.fmt == HX_ROWS_E4M3)
+    k_qk_forward<T, PU, kInter, HX_ROWS_E4M3><<<grid, kThreads, 0, s>>>(a);
   else
-    k_qk_forward<T, PU, kInter><<<grid, kThreads, 0, s>>>(a);
+    k_qk_forward<T, PU, kInter, HX_ROWS_INT8><<<grid, kThreads, 0, s>>>(a);
   return launched();
 }
 template <typename T, int PU>
@@ -633,7 +627,7 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
     blocks = q + k;
     if (const int rc = run(true, p->dtype, pu, p->interleaved != 0, a, blocks, s)) return rc;
   }
-  k_qk_weights<<<dim3((a.dim + 31) / 32, 2), 256, 0, s>>>(a.part, a.dim, a.blocks_q, (uint32_t)blocks,
+  k_qk_weights<<<dim3((a.dim + 31) / 32, 2), 1024, 0, s>>>(a.part, a.dim, a.blocks_q, (uint32_t)blocks,
                                                         d_dwq, d_dwk);
   return launched();
 }

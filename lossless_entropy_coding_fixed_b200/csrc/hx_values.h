@@ -60,6 +60,21 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// max(m, |w|) of both halves.
+template <typename T>
+__device__ __forceinline__ uint32_t top2(uint32_t m, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t top2<__half>(uint32_t m, uint32_t w) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&m), __habs2(*reinterpret_cast<const __half2*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t top2<__nv_bfloat16>(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 r =
+      __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // --------------------------------------------------------------------- W consecutive elements
 // Loaded as they are in memory: 8 or 4 elements of 32 bits, 8, 4 or 2 of 16 bits, or 1 of either. The address is a
 // multiple of min(16, W * sizeof(T)). kRaw: 32-bit registers held.
@@ -91,14 +106,14 @@ struct Vec {
     for (int i = 0; i < kRaw; ++i) r[i] = 0;
   }
   // bits of the largest magnitude so far (as T's bits; NaN and infinities compare above all
-  // finite values), per 16-bit half for 16-bit types
+  // finite values), per 16-bit half for 16-bit types (the packed maximum keeps a NaN)
   __device__ __forceinline__ uint32_t top(uint32_t m) const {
 #pragma unroll
     for (int i = 0; i < kRaw; ++i) {
       if constexpr (sizeof(T) == 4)
         m = max(m, r[i] & 0x7fffffffu);
       else
-        m = __vmaxu2(m, r[i] & 0x7fff7fffu);
+        m = top2<T>(m, r[i]);
     }
     return m;
   }
