@@ -110,13 +110,18 @@ __device__ __forceinline__ void from_slots(int j, const float2 (&v)[8], float (&
   }
 }
 
-__device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
-  for (uint32_t o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Butterflies over a group's lanes: a sum and a maximum, or two sums, in the same rounds.
+__device__ __forceinline__ void group_sum_max(float& v, uint32_t& m, uint32_t lanes) {
+  for (uint32_t o = lanes >> 1; o; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
 }
-__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t lanes) {
-  for (uint32_t o = lanes >> 1; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ void group_sums(float& v, float& w, uint32_t lanes) {
+  for (uint32_t o = lanes >> 1; o; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    w += __shfl_xor_sync(0xffffffffu, w, o);
+  }
 }
 
 template <typename T, int PU, bool kInter>
@@ -215,7 +220,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
   Vec<T, PU> v0[S::N], v1[S::N];
   const T* x = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
   T* y = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
-  uint64_t row = t * (a.nq + a.nk) + h0;
+  const uint64_t row = t * (a.nq + a.nk) + h0;
+  uint8_t* bytes = a.bytes + row * a.dim;
+  float* scale = a.scale + row;
   auto fetch = [&](bool any) {
 #pragma unroll
     for (int j = 0; j < S::N; ++j) {
@@ -259,23 +266,23 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
     fetch(h + 1 < h1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) q = fma2(v[i], v[i], q);
-    const float sq = group_sum(q.x + q.y, a.lanes);
+    float sq = q.x + q.y;
+    if (a.bytes) top = top_bits<T>(top);
+    group_sum_max(sq, top, a.lanes);
     float r = rsqrtf(fmaf(sq, part, a.eps));
     if (!ok) r = __uint_as_float(0x7fc00000u);
     if (a.bytes) {
-      top = group_max(top_bits<T>(top), a.lanes);
       const Scale sc = scale_of<T>(kFmt, top);
       if (h < h1) {
-        if (sub == 0) a.scale[row] = sc.s;
-        uint8_t* b = a.bytes + row * a.dim;
+        if (sub == 0) *scale = sc.s;
 #pragma unroll
         for (int j = 0; j < S::N; ++j) {
           const uint32_t u = j * a.lanes + sub;
           if (!un.has(u)) continue;
           float f0[PU], f1[PU];
           from_slots<PU>(j, v, f0, f1);
-          to_bytes<PU>(kFmt, f0, sc).store(b + un.off0(u));
-          to_bytes<PU>(kFmt, f1, sc).store(b + un.off1(u));
+          to_bytes<PU>(kFmt, f0, sc).store(bytes + un.off0(u));
+          to_bytes<PU>(kFmt, f1, sc).store(bytes + un.off1(u));
         }
       }
     }
@@ -295,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
       }
     }
     y += a.yh;
-    ++row;
+    bytes += a.dim;
+    ++scale;
   }
 }
 
@@ -389,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
         gq[i] = mul2(g[i], q[i]);
         dot2 = fma2(gq[i], w[i], dot2);
       }
-      const float sq = group_sum(sq2.x + sq2.y, a.lanes) * scale * scale;
-      const float dot = group_sum(dot2.x + dot2.y, a.lanes) * scale;
+      float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
+      group_sums(sq, dot, a.lanes);
+      sq *= scale * scale, dot *= scale;
       float r = rsqrtf(fmaf(sq, part, a.eps));
       if (!ok) r = __uint_as_float(0x7fc00000u);
       const float sr = scale * r;                // n = q sr

@@ -234,14 +234,17 @@ template <int W>
 __device__ __forceinline__ Bytes<W> to_bytes(uint32_t fmt, const float (&x)[W], const Scale& sc) {
   Bytes<W> out;
   if (fmt == HX_ROWS_E4M3) {
-    uint32_t h[(W + 1) / 2];
+    if constexpr (W >= 4) {
 #pragma unroll
-    for (int i = 0; i < (W + 1) / 2; ++i) {
-      const float hi = 2 * i + 1 < W ? x[(2 * i + 1) % W] * sc.inv : 0.0f;
-      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * sc.inv, hi), __NV_SATFINITE, __NV_E4M3);
+      for (int i = 0; i < W / 4; ++i)
+        asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+            " mov.b32 %0, {l, h};\n}"
+            : "=r"(out.b[i])
+            : "f"(x[4 * i] * sc.inv), "f"(x[4 * i + 1] * sc.inv), "f"(x[4 * i + 2] * sc.inv), "f"(x[4 * i + 3] * sc.inv));
+    } else {
+      const float hi = W == 2 ? x[W - 1] * sc.inv : 0.0f;
+      out.b[0] = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * sc.inv, hi), __NV_SATFINITE, __NV_E4M3);
     }
-#pragma unroll
-    for (int i = 0; i < Bytes<W>::kRaw; ++i) out.b[i] = W >= 4 ? h[(2 * i) % ((W + 1) / 2)] | h[(2 * i + 1) % ((W + 1) / 2)] << 16 : h[i];
   } else {
     constexpr float kRound = 12582912.0f;
     uint32_t q[W];
@@ -279,13 +282,21 @@ __device__ __forceinline__ Bytes<W> to_bytes(uint32_t fmt, const float (&x)[W], 
 template <int W>
 __device__ __forceinline__ void to_values(uint32_t fmt, const Bytes<W>& in, float s, float (&x)[W]) {
   if (fmt == HX_ROWS_E4M3) {
+    if constexpr (W >= 4) {
 #pragma unroll
-    for (int i = 0; i < (W + 1) / 2; ++i) {
-      const uint32_t two = in.b[i / 2] >> (16 * (i & 1));
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+      for (int i = 0; i < W / 4; ++i) {
+        uint32_t h0, h1;
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+            : "=r"(h0), "=r"(h1)
+            : "r"(in.b[i]));
+        const float2 v0 = unpack2<__half>(h0), v1 = unpack2<__half>(h1);
+        x[4 * i] = v0.x * s, x[4 * i + 1] = v0.y * s, x[4 * i + 2] = v1.x * s, x[4 * i + 3] = v1.y * s;
+      }
+    } else {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in.b[0] & 0xffffu), __NV_E4M3);
       const float2 v = __half22float2(__half2(h));
-      x[2 * i] = v.x * s;
-      if (2 * i + 1 < W) x[(2 * i + 1) % W] = v.y * s;
+      x[0] = v.x * s;
+      if (W == 2) x[W - 1] = v.y * s;
     }
   } else {
     // 2^23 + (byte + 128) from its bits (an integer conversion runs at a quarter of this rate)
