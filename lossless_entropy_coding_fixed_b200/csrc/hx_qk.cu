@@ -194,6 +194,64 @@ __device__ __forceinline__ bool load_turn(const Args& a, uint64_t t, uint32_t su
   return ok;
 }
 
+// ------------------------------------------------------------------------------ loads ahead
+// A thread's vectors of the next heads, on their way through asynchronous copies into slots of shared memory that only
+// this thread reads (so that they need neither registers nor a barrier). B: bytes of one vector, 1 .. 32 (1 and 2 have no
+// asynchronous copy: loaded and stored).
+constexpr int kAhead = 4;
+template <int B>
+__device__ __forceinline__ void copy_ahead(uint32_t slot, const void* p) {
+  if constexpr (B == 32) {
+    copy_ahead<16>(slot, p);
+    copy_ahead<16>(slot + 16 * kThreads, static_cast<const uint8_t*>(p) + 16);
+  } else if constexpr (B == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(p) : "memory");
+  } else if constexpr (B >= 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(slot), "l"(p), "n"(B) : "memory");
+  } else if constexpr (B == 2) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(slot), "h"(*static_cast<const uint16_t*>(p)) : "memory");
+  } else {
+    asm volatile("st.shared.b8 [%0], %1;" ::"r"(slot), "r"((uint32_t)*static_cast<const uint8_t*>(p)) : "memory");
+  }
+}
+__device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void ahead_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+template <typename T, int PU>
+__device__ __forceinline__ void read_ahead(uint32_t slot, Vec<T, PU>& v) {
+  constexpr int B = PU * sizeof(T);
+  if constexpr (B >= 16) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i)
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.r[4 * i]), "=r"(v.r[4 * i + 1]), "=r"(v.r[4 * i + 2]), "=r"(v.r[4 * i + 3])
+                   : "r"(slot + i * 16 * kThreads)
+                   : "memory");
+  } else if constexpr (B == 8) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.r[0]), "=r"(v.r[1]) : "r"(slot) : "memory");
+  } else if constexpr (B == 4) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v.r[0]) : "r"(slot) : "memory");
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(slot) : "memory");
+    v.r[0] = h;
+  }
+}
+
+template <int PU>
+__device__ __forceinline__ void read_ahead(uint32_t slot, Bytes<PU>& v) {
+  if constexpr (PU == 8) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.b[0]), "=r"(v.b[1]) : "r"(slot) : "memory");
+  } else if constexpr (PU == 4) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v.b[0]) : "r"(slot) : "memory");
+  } else if constexpr (PU == 2) {
+    uint16_t h;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(slot) : "memory");
+    v.b[0] = h;
+  } else {
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v.b[0]) : "r"(slot) : "memory");
+  }
+}
+
 // Item i as (token, chunk of heads).
 __device__ __forceinline__ void split_item(uint64_t i, uint32_t chunks, uint64_t& t, uint32_t& ch) {
   t = i >> 32 ? i / chunks : (uint32_t)i / chunks;
@@ -217,27 +275,30 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
   const uint32_t h0 = key ? a.nq + (ch - cq) * a.per : ch * a.per;
   const uint32_t h1 = live ? min(h0 + a.per, key ? a.nq + a.nk : a.nq) : h0;
 
-  Vec<T, PU> v0[S::N], v1[S::N];
+  constexpr int B = PU * sizeof(T), kSlot = 16 * sizeof(T) * kThreads;  // a head's 16 values of every thread
+  extern __shared__ __align__(16) uint8_t ahead[];
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(ahead) + threadIdx.x * (B < 16 ? B : 16);
   const T* x = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
   T* y = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
   const uint64_t row = t * (a.nq + a.nk) + h0;
   uint8_t* bytes = a.bytes + row * a.dim;
   float* scale = a.scale + row;
-  auto fetch = [&](bool any) {
+  // past the item's last head the loads go to that head again; a lane without values reads the head's first ones and
+  // clears them on use
+  const bool idle = un.units < a.lanes * S::N;
+  auto fetch = [&](uint32_t h) {
+    const uint32_t slot = slots + (h - h0) % kAhead * kSlot;
 #pragma unroll
     for (int j = 0; j < S::N; ++j) {
-      const uint32_t u = j * a.lanes + sub;
-      if (any && un.has(u)) {
-        v0[j].load(x + un.off0(u));
-        v1[j].load(x + un.off1(u));
-      } else {
-        v0[j].zero();
-        v1[j].zero();
-      }
+      const uint32_t u = j * a.lanes + sub, v = un.has(u) ? u : 0;
+      copy_ahead<B>(slot + (2 * j) * B * kThreads, x + un.off0(v));
+      copy_ahead<B>(slot + (2 * j + 1) * B * kThreads, x + un.off1(v));
     }
-    x += a.xh;
+    ahead_commit();
+    if (h + 1 < h1) x += a.xh;
   };
-  fetch(h0 < h1);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(h0 + i);
   float2 c[8], s[8];
   bool ok;
   {
@@ -255,15 +316,21 @@ __global__ void __launch_bounds__(kThreads, 3) k_qk_forward(const __grid_constan
     const uint32_t h = h0 + k;
     float2 v[8], q = both(0.0f);
     uint32_t top = 0;
+    ahead_wait();
 #pragma unroll
     for (int j = 0; j < S::N; ++j) {
       float f0[PU], f1[PU];
+      Vec<T, PU> v0[S::N], v1[S::N];
+      const uint32_t slot = slots + k % kAhead * kSlot;
+      read_ahead<T, PU>(slot + (2 * j) * B * kThreads, v0[j]);
+      read_ahead<T, PU>(slot + (2 * j + 1) * B * kThreads, v1[j]);
+      if (idle && !un.has(j * a.lanes + sub)) v0[j].zero(), v1[j].zero();
       v0[j].floats(f0);
       v1[j].floats(f1);
       to_slots<PU>(j, f0, f1, v);
       if (a.bytes) top = v1[j].top(v0[j].top(top));
     }
-    fetch(h + 1 < h1);
+    fetch(h + kAhead);
 #pragma unroll
     for (int i = 0; i < 8; ++i) q = fma2(v[i], v[i], q);
     float sq = q.x + q.y;
@@ -321,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
   const uint32_t blocks = key ? gridDim.x - a.blocks_q : a.blocks_q;
   const uint32_t block = key ? blockIdx.x - a.blocks_q : blockIdx.x;
   const uint64_t items = a.tokens * chunks;
+  const bool idle = un.units < a.lanes * S::N;
   const float part = 1.0f / (float)a.dim;
 
   float2 w[8], dw[8];
@@ -328,61 +396,106 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = both(0.0f);
 
-  for (uint64_t base = (uint64_t)block * groups; base < items; base += (uint64_t)blocks * groups) {
+  // Slots of a head's values of dy, its bytes and its scale, of every thread. The loads run kAhead heads before their use,
+  // through the items in the same order; past an item's last head they go to that head again, past the last item
+  // to that item, and a lane without values reads the head's first ones and clears them on use. (An item that is
+  // not live reads token 0's first head, and stores nothing.)
+  constexpr int B = PU * sizeof(T), kDy = 16 * sizeof(T) * kThreads, kSlot = kDy + 20 * kThreads;
+  extern __shared__ __align__(16) uint8_t ahead[];
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(ahead);
+  const uint32_t slot_x = slots + threadIdx.x * (B < 16 ? B : 16), slot_b = slots + kDy + threadIdx.x * PU;
+  const uint32_t slot_s = slots + kDy + 16 * kThreads + threadIdx.x * 4;
+  struct Item {
+    uint64_t t;
+    uint32_t h0, n;
+  };
+  auto item_at = [&](uint64_t base) {
     const uint64_t item = base + group;
-    const bool live = item < items;
-    uint64_t t = 0;
-    uint32_t ch = 0;
-    if (live) split_item(item, chunks, t, ch);
-    const uint32_t h0 = first + ch * a.per;
-    const uint32_t h1 = live ? min(h0 + a.per, first + heads) : h0;
+    Item it{0, first, 0};
+    if (item < items) {
+      uint32_t ch;
+      split_item(item, chunks, it.t, ch);
+      it.h0 = first + ch * a.per;
+      it.n = min(a.per, first + heads - it.h0);
+    }
+    return it;
+  };
+  const uint64_t step = (uint64_t)blocks * groups;
+  uint64_t at = (uint64_t)block * groups;  // of the loads
+  uint32_t at_k = 0, at_n = 0, slot = 0;
+  const T* dy = nullptr;
+  const uint8_t* bytes = nullptr;
+  const float* scales = nullptr;
+  auto go_to = [&](uint64_t base) {
+    const Item it = item_at(base);
+    const uint64_t row = it.t * (a.nq + a.nk) + it.h0;
+    dy = static_cast<const T*>(a.x) + it.t * a.xt + it.h0 * a.xh;
+    bytes = a.bytes + row * a.dim;
+    scales = a.scale + row;
+    at_n = it.n;
+  };
+  auto fetch = [&]() {
+    const uint32_t o = slot * kSlot;
+    copy_ahead<4>(slot_s + o, scales);
+#pragma unroll
+    for (int j = 0; j < S::N; ++j) {
+      const uint32_t u = j * a.lanes + sub, v = un.has(u) ? u : 0;
+      copy_ahead<B>(slot_x + o + (2 * j) * B * kThreads, dy + un.off0(v));
+      copy_ahead<B>(slot_x + o + (2 * j + 1) * B * kThreads, dy + un.off1(v));
+      copy_ahead<PU>(slot_b + o + (2 * j) * PU * kThreads, bytes + un.off0(v));
+      copy_ahead<PU>(slot_b + o + (2 * j + 1) * PU * kThreads, bytes + un.off1(v));
+    }
+    ahead_commit();
+    slot = (slot + 1) % kAhead;
+    if (++at_k == a.per) {
+      at_k = 0;
+      if (at + step < items) at += step;
+      go_to(at);
+    } else if (at_k < at_n) {
+      dy += a.xh, bytes += a.dim, ++scales;
+    }
+  };
+  if ((uint64_t)block * groups < items) {
+    go_to(at);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch();
+  }
+
+  for (uint64_t base = (uint64_t)block * groups; base < items; base += step) {
+    const Item it = item_at(base);
     float2 c[8], s[8];
-    Vec<T, PU> v0[S::N], v1[S::N];
-    Bytes<PU> b0[S::N], b1[S::N];
-    float sc = 0.0f;
-    const T* dy = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
-    T* dx = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
-    uint64_t row = t * (a.nq + a.nk) + h0;
-    const uint8_t* bytes = a.bytes + row * a.dim;
-    auto fetch = [&](bool any) {
-      sc = any ? a.scale[row] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < S::N; ++j) {
-        const uint32_t u = j * a.lanes + sub;
-        if (any && un.has(u)) {
-          v0[j].load(dy + un.off0(u));
-          v1[j].load(dy + un.off1(u));
-          b0[j].load(bytes + un.off0(u));
-          b1[j].load(bytes + un.off1(u));
-        } else {
-          v0[j].zero();
-          v1[j].zero();
-#pragma unroll
-          for (int i = 0; i < Bytes<PU>::kRaw; ++i) b0[j].b[i] = b1[j].b[i] = 0;
-        }
-      }
-      dy += a.xh;
-      bytes += a.dim;
-      ++row;
-    };
-    fetch(h0 < h1);
-    // (token 0's for an item that is not live: its heads are empty)
-    const bool ok = load_turn<PU, kInter>(a, t, sub, -1.0f, c, s);
+    T* dx = static_cast<T*>(a.y) + it.t * a.yt + it.h0 * a.yh;
+    const bool ok = load_turn<PU, kInter>(a, it.t, sub, -1.0f, c, s);
     for (uint32_t k = 0; k < a.per; ++k) {
-      const uint32_t h = h0 + k;
+      const bool live = k < it.n;
       float2 g[8], q[8];
-      const float scale = sc;
+      ahead_wait();
+      const uint32_t o = slot * kSlot;  // the oldest, and the next to be filled
+      float scale;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(slot_s + o) : "memory");
 #pragma unroll
       for (int j = 0; j < S::N; ++j) {
         float f0[PU], f1[PU];
-        v0[j].floats(f0);
-        v1[j].floats(f1);
+        Vec<T, PU> v0, v1;
+        Bytes<PU> b0, b1;
+        read_ahead<T, PU>(slot_x + o + (2 * j) * B * kThreads, v0);
+        read_ahead<T, PU>(slot_x + o + (2 * j + 1) * B * kThreads, v1);
+        read_ahead<PU>(slot_b + o + (2 * j) * PU * kThreads, b0);
+        read_ahead<PU>(slot_b + o + (2 * j + 1) * PU * kThreads, b1);
+        if (idle && !un.has(j * a.lanes + sub)) {
+          v0.zero();
+          v1.zero();
+#pragma unroll
+          for (int i = 0; i < Bytes<PU>::kRaw; ++i) b0.b[i] = b1.b[i] = 0;
+        }
+        v0.floats(f0);
+        v1.floats(f1);
         to_slots<PU>(j, f0, f1, g);
-        to_values<PU>(kFmt, b0[j], 1.0f, f0);
-        to_values<PU>(kFmt, b1[j], 1.0f, f1);
+        to_values<PU>(kFmt, b0, 1.0f, f0);
+        to_values<PU>(kFmt, b1, 1.0f, f1);
         to_slots<PU>(j, f0, f1, q);
       }
-      fetch(h + 1 < h1);
+      fetch();
       {
         float2 o[8];
 #pragma unroll
@@ -404,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
       if (!ok) r = __uint_as_float(0x7fc00000u);
       const float sr = scale * r;                // n = q sr
       const float2 m = both(-dot * r * part * sr * r);  // dx = g w r - q (mean(g w n) s r r)
-      if (h < h1) {
+      if (live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           dw[i] = fma2(gq[i], both(sr), dw[i]);
@@ -494,17 +607,19 @@ int vector_of(const Args& a, uint64_t e) {
   return 1;
 }
 
+int launch_ahead(void (*kernel)(const Args), uint64_t smem, const Args& a, uint32_t grid, cudaStream_t s) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return HX_ERR_CUDA;
+  kernel<<<grid, kThreads, smem, s>>>(a);
+  return launched();
+}
+
 template <typename T, int PU, bool kInter>
 int launch(bool backward, const Args& a, uint32_t grid, cudaStream_t s) {
-  if (backward && a.fmt == HX_ROWS_E4M3)
-    k_qk_backward<T, PU, kInter, HX_ROWS_E4M3><<<grid, kThreads, 0, s>>>(a);
-  else if (backward)
-    k_qk_backward<T, PU, kInter, HX_ROWS_INT8><<<grid, kThreads, 0, s>>>(a);
-  else if (a.fmt == HX_ROWS_E4M3)
-    k_qk_forward<T, PU, kInter, HX_ROWS_E4M3><<<grid, kThreads, 0, s>>>(a);
-  else
-    k_qk_forward<T, PU, kInter, HX_ROWS_INT8><<<grid, kThreads, 0, s>>>(a);
-  return launched();
+  constexpr uint64_t fwd = 16 * sizeof(T) * kThreads * kAhead, bwd = fwd + 20 * kThreads * kAhead;
+  if (backward && a.fmt == HX_ROWS_E4M3) return launch_ahead(k_qk_backward<T, PU, kInter, HX_ROWS_E4M3>, bwd, a, grid, s);
+  if (backward) return launch_ahead(k_qk_backward<T, PU, kInter, HX_ROWS_INT8>, bwd, a, grid, s);
+  if (a.fmt == HX_ROWS_E4M3) return launch_ahead(k_qk_forward<T, PU, kInter, HX_ROWS_E4M3>, fwd, a, grid, s);
+  return launch_ahead(k_qk_forward<T, PU, kInter, HX_ROWS_INT8>, fwd, a, grid, s);
 }
 template <typename T, int PU>
 int launch_style(bool backward, bool inter, const Args& a, uint32_t grid, cudaStream_t s) {
