@@ -14,6 +14,7 @@
 // norm one butterfly over L lanes. A group takes up to 8 heads of one token one after another, with
 // the token's cosines and sines and the weight in registers and the next head's loads in flight.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "hx.h"
@@ -46,6 +47,7 @@ struct Args {
   uint32_t* status;
   uint32_t lanes, per;  // lanes per head, heads per item
   float* part;          // backward: [blocks][dim]
+  float *dwq, *dwk;     // backward, with one block each at most: written by it
   uint32_t blocks_q;    // backward: the first blocks take queries, the others keys
 };
 
@@ -555,7 +557,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
   for (uint32_t d = threadIdx.x; d < a.dim; d += kThreads) {
     float v = 0.0f;
     for (uint32_t g = 0; g < groups; ++g) v += sums[g * (16 * a.lanes) + d];
-    a.part[(uint64_t)blockIdx.x * a.dim + d] = v;
+    if (blocks == 1)
+      (key ? a.dwk : a.dwq)[d] = v;
+    else
+      a.part[(uint64_t)blockIdx.x * a.dim + d] = v;
   }
 }
 
@@ -568,6 +573,7 @@ __global__ void __launch_bounds__(1024) k_qk_weights(const float* __restrict__ p
   const uint32_t x = threadIdx.x & 31, k = threadIdx.x >> 5, d = blockIdx.x * 32 + x;
   const uint32_t lo = blockIdx.y ? blocks_q : 0, hi = blockIdx.y ? blocks : blocks_q;
   float* dw = blockIdx.y ? dwk : dwq;
+  if (hi - lo == 1) return;  // written by its one block
   float v = 0.0f;
   if (d < dim) {
 #pragma unroll 8
@@ -585,10 +591,14 @@ __global__ void __launch_bounds__(1024) k_qk_weights(const float* __restrict__ p
 int launched() { return cudaGetLastError() == cudaSuccess ? HX_OK : HX_ERR_CUDA; }
 bool multiple(const void* p, uint64_t of) { return (reinterpret_cast<uintptr_t>(p) % of) == 0; }
 
+// SMs of the current device, 0 on an error; asked for once per device.
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -607,8 +617,9 @@ int vector_of(const Args& a, uint64_t e) {
   return 1;
 }
 
-int launch_ahead(void (*kernel)(const Args), uint64_t smem, const Args& a, uint32_t grid, cudaStream_t s) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return HX_ERR_CUDA;
+template <void (*kernel)(const Args)>
+int launch_ahead(uint64_t smem, const Args& a, uint32_t grid, cudaStream_t s) {
+  if (!allow_shared<kernel>((int)smem)) return HX_ERR_CUDA;
   kernel<<<grid, kThreads, smem, s>>>(a);
   return launched();
 }
@@ -616,10 +627,10 @@ int launch_ahead(void (*kernel)(const Args), uint64_t smem, const Args& a, uint3
 template <typename T, int PU, bool kInter>
 int launch(bool backward, const Args& a, uint32_t grid, cudaStream_t s) {
   constexpr uint64_t fwd = 16 * sizeof(T) * kThreads * kAhead, bwd = fwd + 20 * kThreads * kAhead;
-  if (backward && a.fmt == HX_ROWS_E4M3) return launch_ahead(k_qk_backward<T, PU, kInter, HX_ROWS_E4M3>, bwd, a, grid, s);
-  if (backward) return launch_ahead(k_qk_backward<T, PU, kInter, HX_ROWS_INT8>, bwd, a, grid, s);
-  if (a.fmt == HX_ROWS_E4M3) return launch_ahead(k_qk_forward<T, PU, kInter, HX_ROWS_E4M3>, fwd, a, grid, s);
-  return launch_ahead(k_qk_forward<T, PU, kInter, HX_ROWS_INT8>, fwd, a, grid, s);
+  if (backward && a.fmt == HX_ROWS_E4M3) return launch_ahead<k_qk_backward<T, PU, kInter, HX_ROWS_E4M3>>(bwd, a, grid, s);
+  if (backward) return launch_ahead<k_qk_backward<T, PU, kInter, HX_ROWS_INT8>>(bwd, a, grid, s);
+  if (a.fmt == HX_ROWS_E4M3) return launch_ahead<k_qk_forward<T, PU, kInter, HX_ROWS_E4M3>>(fwd, a, grid, s);
+  return launch_ahead<k_qk_forward<T, PU, kInter, HX_ROWS_INT8>>(fwd, a, grid, s);
 }
 template <typename T, int PU>
 int launch_style(bool backward, bool inter, const Args& a, uint32_t grid, cudaStream_t s) {
@@ -748,8 +759,11 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
       k = bk ? most - q : 0;
     }
     a.blocks_q = (uint32_t)q;
+    a.dwq = d_dwq, a.dwk = d_dwk;
     blocks = q + k;
     if (const int rc = run(true, p->dtype, pu, p->interleaved != 0, a, blocks, s)) return rc;
+    // a class with one block has its sums; one without heads has none to write
+    if (q <= 1 && k <= 1 && (q || !d_dwq) && (k || !d_dwk)) return HX_OK;
   }
   k_qk_weights<<<dim3((a.dim + 31) / 32, 2), 1024, 0, s>>>(a.part, a.dim, a.blocks_q, (uint32_t)blocks,
                                                         d_dwq, d_dwk);

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "hx.h"
 
 namespace hxv {
@@ -306,6 +308,23 @@ __device__ __forceinline__ void to_values(uint32_t fmt, const Bytes<W>& in, floa
       x[i] = __fsub_rn(__uint_as_float(f), 8388736.0f) * s;
     }
   }
+}
+
+// --------------------------------------------------------------------------------------- host
+// Allows `kernel` `bytes` of dynamic shared memory on the current device: asked for once per device.
+template <auto kernel>
+inline bool allow_shared(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 }  // namespace hxv

@@ -687,8 +687,7 @@ template <typename T, int MT, bool kPair, int kParts>
 int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
   using S = Tile<MT, kPair, kParts>;
   const auto kernel = k_wgrad<T, MT, kPair, kParts>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
-    return HX_ERR_CUDA;
+  if (!allow_shared<k_wgrad<T, MT, kPair, kParts>>(S::kSmem)) return HX_ERR_CUDA;
   const uint64_t ctas = ceil_div(a.n_out, S::BM) * ceil_div(a.n_in, S::BN) * S::kCtas * a.splits;
   if (ctas >= (1ull << 31)) return HX_ERR_ARG;
   cudaLaunchConfig_t c{};

@@ -551,8 +551,8 @@ def _device(t, what) -> int:
     return t.get_device()
 
 
-def _same(t, what, shape, dtype, dev):
-    """Checks a tensor's device, element type and shape."""
+def _refuse(t, what, shape, dtype, dev):
+    """Raises what is wrong with a tensor that should have this shape, element type and device."""
     if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
     if t.dtype is not dtype:
@@ -561,13 +561,20 @@ def _same(t, what, shape, dtype, dev):
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{what} is on another device than the other tensors")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _same(t, what, shape, dtype, dev):
+    """Checks a tensor's device, element type and shape."""
+    if not isinstance(t, _torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, what, shape, dtype, dev)
 
 
 def _dense(t, what, shape, dtype, dev) -> int:
     """Checks a contiguous tensor; its address."""
-    _same(t, what, shape, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if (not isinstance(t, _torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, what, shape, dtype, dev)
     return t.data_ptr()
 
 
@@ -620,7 +627,7 @@ def dequantize_rows(data, scale, fmt: int = ROWS_E4M3, dtype=None, out=None):
     db = _dense(data, "bytes", shape, torch.uint8, dev)
     sp = _dense(scale, "scale", shape[:1], torch.float32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=data.device)
+        out = torch.empty(*shape, dtype=dtype or torch.bfloat16, device=data.device)
     else:
         _same(out, "out", shape, dtype or out.dtype, dev)
     rows, cols, ld = _matrix(out, "out")
@@ -733,14 +740,14 @@ def head_norm_rope_forward(x, q_heads: int, wq, wk, cos, sin, positions, eps: fl
     p = _head_norm_rope(x, dev, dt, q_heads, wq, wk, cos, sin, positions, eps, interleaved, fmt)
     shape = x.shape
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(*shape, dtype=x.dtype, device=x.device)
         yt, yh = out.stride()[:2]
     else:
         yt, yh = _heads_out(out, shape, x.dtype, dev)
     data = scale = db = sp = None
     if save:
-        data = torch.empty(shape, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(shape[:2], dtype=torch.float32, device=x.device)
+        data = torch.empty(*shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(*shape[:2], dtype=torch.float32, device=x.device)
         db, sp = data.data_ptr(), scale.data_ptr()
     _launch(dev, "hx_head_norm_rope_forward", lib().hx_head_norm_rope_forward, p, x.data_ptr(), xt, xh, out.data_ptr(),
             yt, yh, db, sp, _status_ptr(status, dev))
@@ -760,7 +767,7 @@ def head_norm_rope_backward(dy, data, scale, q_heads: int, wq, wk, cos, sin, pos
     db = _dense(data, "bytes", shape, torch.uint8, dev)
     sp = _dense(scale, "scale", shape[:2], torch.float32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        out = torch.empty(*shape, dtype=dy.dtype, device=dy.device)
         ot, oh = out.stride()[:2]
     else:
         ot, oh = _heads_out(out, shape, dy.dtype, dev)
