@@ -51,18 +51,20 @@ struct Args {
   uint32_t blocks_q;    // backward: the first blocks take queries, the others keys
 };
 
-// The places of a lane's values: unit j of the lane is vectors of PU values at off0 and off1, whose
-// pairs have the angles PU u .. PU u + PU - 1 of the token.
+// The places of a lane's values: unit u is two vectors of PU values at off0 and off1. Pairs half the rotated width
+// apart: the two vectors of a turned unit hold them, with the angles PU u ..; vectors behind the rotated ones are
+// neighbours. Interleaved pairs lie inside a vector, so its two vectors are half the head apart (the lanes' vectors are
+// then neighbours, and a warp's loads and stores whole lines), each with the angles off / 2 ..; vectors of one value: the pair.
 template <int PU, bool kInter>
 struct Units {
-  uint32_t units, turned, half;
+  static constexpr bool kApart = kInter && PU > 1;
+  uint32_t units, turned, half, far, rot;
   __device__ Units(const Args& a)
-      : units(a.dim / (2 * PU)), turned(a.rot / (2 * PU)), half(a.rot / 2) {}
+      : units(a.dim / (2 * PU)), turned(a.rot / (2 * PU)), half(a.rot / 2), far(a.dim / 2), rot(a.rot) {}
   __device__ bool has(uint32_t u) const { return u < units; }
-  __device__ bool turns(uint32_t u) const { return u < turned; }
-  __device__ uint32_t off0(uint32_t u) const { return kInter || u >= turned ? 2 * PU * u : PU * u; }
+  __device__ uint32_t off0(uint32_t u) const { return kApart || (!kInter && u < turned) ? PU * u : 2 * PU * u; }
   __device__ uint32_t off1(uint32_t u) const {
-    return kInter || u >= turned ? 2 * PU * u + PU : half + PU * u;
+    return kApart ? far + PU * u : !kInter && u < turned ? half + PU * u : 2 * PU * u + PU;
   }
 };
 
@@ -170,7 +172,26 @@ __device__ __forceinline__ bool load_turn(const Args& a, uint64_t t, uint32_t su
     float fc[PU], fs[PU];
 #pragma unroll
     for (int i = 0; i < PU; ++i) fc[i] = 1.0f, fs[i] = 0.0f;
-    if (ok && un.turns(u)) {
+    if constexpr (Units<PU, kInter>::kApart) {
+      // half a vector of pairs in each
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t off = k ? un.off1(u) : un.off0(u);
+        if (ok && un.has(u) && off < un.rot) {
+          const uint64_t at = (uint64_t)p * un.half + off / 2;
+          float g[PU / 2];
+          Vec<float, PU / 2> v;
+          v.load(a.cos + at);
+          v.floats(g);
+#pragma unroll
+          for (int i = 0; i < PU / 2; ++i) fc[k * (PU / 2) + i] = g[i];
+          v.load(a.sin + at);
+          v.floats(g);
+#pragma unroll
+          for (int i = 0; i < PU / 2; ++i) fs[k * (PU / 2) + i] = g[i];
+        }
+      }
+    } else if (ok && u < un.turned) {
       const uint64_t at = (uint64_t)p * un.half + PU * u;
       Vec<float, PU> v;
       v.load(a.cos + at);
@@ -603,13 +624,13 @@ int sm_count() {
 }
 
 // Values per vector: the widest with which every vector of every head starts on its own boundary.
-int vector_of(const Args& a, uint64_t e) {
+int vector_of(const Args& a, uint64_t e, bool inter) {
   for (int pu = 8; pu > 1; pu /= 2) {
     const uint64_t al = std::min<uint64_t>(16, pu * e), fl = std::min<uint64_t>(16, pu * 4);
     const bool strides = (a.xt * e) % al == 0 && (a.xh * e) % al == 0 && (a.yt * e) % al == 0 &&
                          (a.yh * e) % al == 0;
     const uint64_t wl = a.w_f32 ? fl : al;
-    if (a.dim % (2 * pu) == 0 && a.rot % (2 * pu) == 0 && strides && multiple(a.x, al) &&
+    if (a.dim % (2 * pu) == 0 && a.rot % (inter ? pu : 2 * pu) == 0 && strides && multiple(a.x, al) &&
         multiple(a.y, al) && multiple(a.bytes, pu) && multiple(a.cos, fl) && multiple(a.sin, fl) &&
         multiple(a.wq, wl) && multiple(a.wk, wl))
       return pu;
@@ -709,7 +730,7 @@ int hx_head_norm_rope_forward(const hx_head_norm_rope* p, const void* d_x, uint6
   if (!a.tokens) return HX_OK;
   const int sms = sm_count();
   if (!sms) return HX_ERR_CUDA;
-  const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2);
+  const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2, p->interleaved != 0);
   arrange(&a, pu, sms);
   const uint64_t items = a.tokens * (ceil_div(a.nq, a.per) + ceil_div(a.nk, a.per));
   return run(false, p->dtype, pu, p->interleaved != 0, a, ceil_div(items, kThreads / a.lanes),
@@ -745,7 +766,7 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
   a.part = static_cast<float*>(d_workspace);
   uint64_t blocks = 0;
   if (a.tokens) {
-    const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2);
+    const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2, p->interleaved != 0);
     arrange(&a, pu, sms);
     // two blocks per SM hold all groups that fit at once; queries and keys share them by heads
     const uint64_t groups = kThreads / a.lanes;

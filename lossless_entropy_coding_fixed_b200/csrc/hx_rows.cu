@@ -3,14 +3,16 @@
 // codes them. The kernels here make the rows (from a matrix, or inside the gated activation) and
 // read them back (as values, or inside the gated activation's backward pass).
 //
-// All are bound by memory: every input is read once and every output written once.
+// All are bound by memory: every input is read once and every output written once. A value's unit is W neighbours of a
+// row: 8 (16-bit types) or 4 where every row starts on their boundary, else 4, 2 or 1.
 //
 //   k_quantize     a row's largest magnitude decides its scale, so the row is held in registers
-//                  between the two: one warp per row of up to 32 * R units, one block per row up
-//                  to 512 * R, and a second read (from L2) of rows longer than that.
+//                  between the two: R units per thread, 1 to 32 lanes per row, one block per row up
+//                  to 512 threads, and a second read (from L2) of rows longer than that.
 //   k_gated_save   the same over a row's gate half and up half, with silu(gate) * up on the way.
 //   k_gated, k_gated_backward, k_dequantize
-//                  the scales are known (or not needed): one unit per thread, no row structure.
+//                  the scales are known (or not needed): U units per thread of a group of 1 to 32 lanes, the loads
+//                  of all before the first is used.
 #include <algorithm>
 #include <cstdint>
 
@@ -32,17 +34,24 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   return __reduce_max_sync(0xffffffffu, m);
 }
 
+// The largest over the lanes of a row: a block's, or `n` (a power of two up to 32) neighbouring lanes'.
+template <bool kBlock>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t n) {
+  if (kBlock) return block_max(m);
+  if (n == 32) return __reduce_max_sync(0xffffffffu, m);
+  for (uint32_t o = n >> 1; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
 // ----------------------------------------------------------------------------------- quantise
-template <typename T, int W, int R, bool kBlock, bool kLong>
+template <typename T, int W, int R, bool kBlock, bool kLong, uint32_t fmt>
 __global__ void __launch_bounds__(512)
-    k_quantize(uint32_t fmt, const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
-               uint8_t* __restrict__ bytes, float* __restrict__ scale) {
-  const uint32_t lane = kBlock ? threadIdx.x : threadIdx.x & 31;
-  const uint32_t n = kBlock ? blockDim.x : 32;
-  const uint64_t row =
-      kBlock ? blockIdx.x : blockIdx.x * (uint64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= rows) return;  // a whole warp (a whole block has a row)
-  const uint32_t units = cols / W;
+    k_quantize(const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
+               uint8_t* __restrict__ bytes, float* __restrict__ scale, uint32_t lanes) {
+  const uint32_t n = kBlock ? blockDim.x : lanes;
+  const uint32_t lane = kBlock ? threadIdx.x : threadIdx.x & (n - 1);
+  const uint64_t row = kBlock ? blockIdx.x : (blockIdx.x * (uint64_t)blockDim.x + threadIdx.x) >> (31 - __clz(n));
+  const uint32_t units = row < rows ? cols / W : 0;  // a warp's last rows may not exist
   const T* xr = x + row * ld;
   uint8_t* br = bytes + row * cols;
   Vec<T, W> v[R];
@@ -59,10 +68,13 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int r = 0; r < R; ++r) m = v[r].top(m);
   }
-  m = top_bits<T>(m);
-  m = kBlock ? block_max(m) : __reduce_max_sync(0xffffffffu, m);
+  m = row_max<kBlock>(top_bits<T>(m), n);
+  if (!kLong) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r].pin();
+  }
   const Scale sc = scale_of<T>(fmt, m);
-  if (lane == 0) scale[row] = sc.s;
+  if (lane == 0 && units) scale[row] = sc.s;
   for (uint32_t base = 0; base < (kLong ? units : 1u); base += R * n) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -87,16 +99,14 @@ __device__ __forceinline__ void gate(const float (&g)[W], const float (&u)[W], f
   for (int i = 0; i < W; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
 }
 
-template <typename T, int W, int R, bool kBlock, bool kLong>
+template <typename T, int W, int R, bool kBlock, bool kLong, uint32_t fmt>
 __global__ void __launch_bounds__(512)
-    k_gated_save(uint32_t fmt, const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
-                 T* __restrict__ out, uint8_t* __restrict__ bytes, float* __restrict__ scale) {
-  const uint32_t lane = kBlock ? threadIdx.x : threadIdx.x & 31;
-  const uint32_t n = kBlock ? blockDim.x : 32;
-  const uint64_t row =
-      kBlock ? blockIdx.x : blockIdx.x * (uint64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const uint32_t units = cols / W;
+    k_gated_save(const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
+                 T* __restrict__ out, uint8_t* __restrict__ bytes, float* __restrict__ scale, uint32_t lanes) {
+  const uint32_t n = kBlock ? blockDim.x : lanes;
+  const uint32_t lane = kBlock ? threadIdx.x : threadIdx.x & (n - 1);
+  const uint64_t row = kBlock ? blockIdx.x : (blockIdx.x * (uint64_t)blockDim.x + threadIdx.x) >> (31 - __clz(n));
+  const uint32_t units = row < rows ? cols / W : 0;
   const T *gr = x + row * ld, *ur = gr + cols;
   uint8_t *bg = bytes + 2 * row * cols, *bu = bg + cols;
   T* hr = out + row * cols;
@@ -117,17 +127,15 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int r = 0; r < R; ++r) mg = g[r].top(mg), mu = u[r].top(mu);
   }
-  mg = top_bits<T>(mg), mu = top_bits<T>(mu);
-  if (kBlock) {
-    mg = block_max(mg);
-    __syncthreads();
-    mu = block_max(mu);
-  } else {
-    mg = __reduce_max_sync(0xffffffffu, mg);
-    mu = __reduce_max_sync(0xffffffffu, mu);
+  mg = row_max<kBlock>(top_bits<T>(mg), n);
+  if (kBlock) __syncthreads();
+  mu = row_max<kBlock>(top_bits<T>(mu), n);
+  if (!kLong) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) g[r].pin(), u[r].pin();
   }
   const Scale sg = scale_of<T>(fmt, mg), su = scale_of<T>(fmt, mu);
-  if (lane == 0) scale[2 * row] = sg.s, scale[2 * row + 1] = su.s;
+  if (lane == 0 && units) scale[2 * row] = sg.s, scale[2 * row + 1] = su.s;
   for (uint32_t base = 0; base < (kLong ? units : 1u); base += R * n) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -149,65 +157,76 @@ __global__ void __launch_bounds__(512)
 }
 
 // ------------------------------------------------------------------- kernels without rows
-// Unit i of the whole matrix as (row, first column); 32-bit division where the count allows.
-struct Place {
-  uint64_t row;
-  uint32_t col;
-};
-template <int W>
-__device__ __forceinline__ Place place_of(uint64_t i, uint32_t units) {
-  Place p;
-  if (i >> 32)
-    p.row = i / units;
-  else
-    p.row = (uint32_t)i / units;
-  p.col = (uint32_t)(i - p.row * units) * W;
-  return p;
-}
-
 constexpr int kFlatThreads = 256;
 
-template <typename T, int W>
-__global__ void __launch_bounds__(kFlatThreads)
-    k_gated(const T* __restrict__ x, uint64_t n, uint32_t cols, uint64_t ld, T* __restrict__ out) {
-  const uint64_t i = blockIdx.x * (uint64_t)kFlatThreads + threadIdx.x;
-  if (i >= n) return;
-  const Place p = place_of<W>(i, cols / W);
-  Vec<T, W> g, u;
-  const T* gr = x + p.row * ld + p.col;
-  g.load(gr);
-  u.load(gr + cols);
-  float fg[W], fu[W], h[W];
-  g.floats(fg);
-  u.floats(fu);
-  gate(fg, fu, h);
-  store<T, W>(out + p.row * cols + p.col, h);
+// A thread's U units of a row: first, first + n, ... `n` lanes (a power of two) share a task of n * U units, `per_row` tasks a row.
+struct Task {
+  uint64_t row;
+  uint32_t first, units;  // of the row; 0 where there is no such row
+};
+struct Tasks {
+  uint64_t rows;
+  uint32_t cols, n, shift, per_row;  // n = 1 << shift
+};
+template <int W, int U>
+__device__ __forceinline__ Task task_of(const Tasks& t) {
+  const uint64_t id = (blockIdx.x * (uint64_t)kFlatThreads + threadIdx.x) >> t.shift;
+  Task k;
+  k.row = id >> 32 ? id / t.per_row : (uint32_t)id / t.per_row;
+  k.first = (uint32_t)(id - k.row * t.per_row) * (t.n * U) + (threadIdx.x & (t.n - 1));
+  k.units = k.row < t.rows ? t.cols / W : 0;
+  return k;
 }
 
-// U units per thread, a block's width apart: four loads of 8 bytes on their way per thread keep the memory busy
-// (8192 x 8192 to bf16: 41.0 us with one, 34.9 with two, 33.3 with four; 201 MB at the measured copy rate are 30.7).
 template <typename T, int W, int U>
 __global__ void __launch_bounds__(kFlatThreads)
-    k_dequantize(uint32_t fmt, const uint8_t* __restrict__ bytes, const float* __restrict__ scale,
-                 uint64_t n, uint32_t cols, T* __restrict__ out, uint64_t ld) {
-  const uint64_t i0 = blockIdx.x * (uint64_t)(U * kFlatThreads) + threadIdx.x;
-  Bytes<W> b[U];
-  float s[U];
-  Place p[U];
+    k_gated(const T* __restrict__ x, const Tasks t, uint64_t ld, T* __restrict__ out) {
+  const Task k = task_of<W, U>(t);
+  const T* gr = x + k.row * ld;
+  Vec<T, W> g[U], u[U];
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const uint64_t i = i0 + k * kFlatThreads;
-    if (i < n) {
-      p[k] = place_of<W>(i, cols / W);
-      b[k].load(bytes + p[k].row * cols + p[k].col);
-      s[k] = scale[p[k].row];
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v < k.units) {
+      g[i].load(gr + (uint64_t)v * W);
+      u[i].load(gr + t.cols + (uint64_t)v * W);
     }
   }
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    if (i0 + k * kFlatThreads >= n) return;
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v >= k.units) return;
+    float fg[W], fu[W], h[W];
+    g[i].floats(fg);
+    u[i].floats(fu);
+    gate(fg, fu, h);
+    store<T, W>(out + k.row * t.cols + (uint64_t)v * W, h);
+  }
+}
+
+// With four loads on their way per thread (8192 x 8192 to bf16: 41.0 us with one, 34.9 with two, 33.1 with four; 201 MB
+// at the measured copy rate are 30.7).
+template <typename T, int W, int U>
+__global__ void __launch_bounds__(kFlatThreads)
+    k_dequantize(uint32_t fmt, const uint8_t* __restrict__ bytes, const float* __restrict__ scale, const Tasks t,
+                 T* __restrict__ out, uint64_t ld) {
+  const Task k = task_of<W, U>(t);
+  if (k.first >= k.units) return;
+  const uint8_t* br = bytes + k.row * t.cols;
+  T* o = out + k.row * ld;
+  Bytes<W> b[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v < k.units) b[i].load(br + (uint64_t)v * W);
+  }
+  const float s = scale[k.row];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v >= k.units) return;
     float f[W];
-    to_values<W>(fmt, b[k], s[k], f);
+    to_values<W>(fmt, b[i], s, f);
     if constexpr (sizeof(T) == 2) {
       if (Type<T>::kInf == Type<__half>::kInf) {
         // a value just below 65504 can round up in its byte: stay finite. (min and max would drop a NaN.)
@@ -216,41 +235,52 @@ __global__ void __launch_bounds__(kFlatThreads)
           f[j] = f[j] > 65504.0f ? 65504.0f : f[j] < -65504.0f ? -65504.0f : f[j];
       }
     }
-    store<T, W>(out + p[k].row * ld + p[k].col, f);
+    store<T, W>(o + (uint64_t)v * W, f);
   }
 }
 
 // h = g p u with p = sigmoid(g): dg = dh u p (1 + g (1 - p)), du = dh g p.
-template <typename T, int W>
+template <typename T, int W, int U>
 __global__ void __launch_bounds__(kFlatThreads)
-    k_gated_backward(uint32_t fmt, const T* __restrict__ dh, uint64_t ld,
-                     const uint8_t* __restrict__ bytes, const float* __restrict__ scale, uint64_t n,
-                     uint32_t cols, T* __restrict__ dx, T* __restrict__ h) {
-  const uint64_t i = blockIdx.x * (uint64_t)kFlatThreads + threadIdx.x;
-  if (i >= n) return;
-  const Place p = place_of<W>(i, cols / W);
-  Vec<T, W> d;
-  Bytes<W> bg, bu;
-  d.load(dh + p.row * ld + p.col);
-  bg.load(bytes + 2 * p.row * cols + p.col);
-  bu.load(bytes + (2 * p.row + 1) * cols + p.col);
-  const float sg = scale[2 * p.row], su = scale[2 * p.row + 1];
-  float fd[W], fg[W], fu[W], fh[W];
-  d.floats(fd);
-  to_values<W>(fmt, bg, sg, fg);
-  to_values<W>(fmt, bu, su, fu);
+    k_gated_backward(uint32_t fmt, const T* __restrict__ dh, uint64_t ld, const uint8_t* __restrict__ bytes,
+                     const float* __restrict__ scale, const Tasks t, T* __restrict__ dx, T* __restrict__ h) {
+  const Task k = task_of<W, U>(t);
+  if (k.first >= k.units) return;
+  const T* dr = dh + k.row * ld;
+  const uint8_t* br = bytes + 2 * k.row * t.cols;
+  Vec<T, W> d[U];
+  Bytes<W> bg[U], bu[U];
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    const float s = sigmoid(fg[j]), silu = fg[j] * s;
-    fh[j] = silu * fu[j];
-    // dg into fu, du into fd
-    fu[j] *= fd[j] * fmaf(silu, 1.0f - s, s);
-    fd[j] *= silu;
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v < k.units) {
+      d[i].load(dr + (uint64_t)v * W);
+      bg[i].load(br + (uint64_t)v * W);
+      bu[i].load(br + t.cols + (uint64_t)v * W);
+    }
   }
-  T* o = dx + 2 * p.row * cols + p.col;
-  store<T, W>(o, fu);
-  store<T, W>(o + cols, fd);
-  if (h) store<T, W>(h + p.row * cols + p.col, fh);
+  const float sg = scale[2 * k.row], su = scale[2 * k.row + 1];
+  T* o = dx + 2 * k.row * t.cols;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t v = k.first + i * t.n;
+    if (v >= k.units) return;
+    float fd[W], fg[W], fu[W], fh[W];
+    d[i].floats(fd);
+    to_values<W>(fmt, bg[i], sg, fg);
+    to_values<W>(fmt, bu[i], su, fu);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float s = sigmoid(fg[j]), silu = fg[j] * s;
+      fh[j] = silu * fu[j];
+      // dg into fu, du into fd
+      fu[j] *= fd[j] * fmaf(silu, 1.0f - s, s);
+      fd[j] *= silu;
+    }
+    store<T, W>(o + (uint64_t)v * W, fu);
+    store<T, W>(o + t.cols + (uint64_t)v * W, fd);
+    if (h) store<T, W>(h + k.row * t.cols + (uint64_t)v * W, fh);
+  }
 }
 
 // ------------------------------------------------------------------------------------- launch
@@ -266,63 +296,97 @@ bool bad_shape(uint32_t fmt, uint32_t dtype, uint64_t rows, uint64_t cols) {
          rows >= (1ull << 31) || (rows && cols > (1ull << 40) / rows);
 }
 
-// Units of 8 values where every row starts on their boundary, else of one.
-bool wide(uint32_t dtype, uint64_t cols, uint64_t ld, const void* a, const void* b,
-          const void* bytes) {
-  const uint64_t e = size_of(dtype), step = 16 / e;
-  return cols % 8 == 0 && ld % step == 0 && multiple(a, 16) && multiple(b, 16) &&
-         multiple(bytes, 8);
+// The widest unit on whose boundary every row of the operands starts (a unit of a 32-bit type is at most 4 values: 16
+// bytes, so that a warp's loads are whole lines).
+int unit_of(uint32_t dtype, uint64_t cols, uint64_t ld, const void* a, const void* b, const void* bytes) {
+  const uint64_t e = size_of(dtype);
+  for (int w = e == 4 ? 4 : 8; w > 1; w /= 2)
+    if (cols % w == 0 && ld % w == 0 && multiple(a, w * e) && multiple(b, w * e) && multiple(bytes, w)) return w;
+  return 1;
 }
 
-// The block and grid of a kernel with a row per warp or block, R units of a row per thread.
+uint32_t power_of_two(uint64_t v) {
+  uint32_t p = 1;
+  while (p < v) p *= 2;
+  return p;
+}
+
+// The block and grid of a kernel that holds a row: R units per thread, as many lanes per row as that takes.
 struct RowLaunch {
   bool block, twice;
-  uint32_t threads, grid;
+  uint32_t threads, lanes;
+  uint64_t grid;
 };
 RowLaunch row_launch(uint64_t rows, uint64_t units, int R) {
   RowLaunch l{};
   l.block = units > 32u * R;
   l.twice = units > 512u * R;
   l.threads = 256;
-  l.grid = (uint32_t)((rows + 7) / 8);
   if (l.block) {
     const uint64_t per = (units + R - 1) / R;
     l.threads = (uint32_t)std::min<uint64_t>(512, (per + 31) / 32 * 32);
-    l.grid = (uint32_t)rows;
+    l.grid = rows;
+  } else {
+    l.lanes = power_of_two((units + R - 1) / R);
+    l.grid = (rows * l.lanes + l.threads - 1) / l.threads;
   }
   return l;
 }
 
-template <typename T, int W, int R>
-int quantize_w(uint32_t fmt, const void* x, uint64_t rows, uint64_t cols, uint64_t ld,
+template <typename T, int W, int R, uint32_t F>
+int quantize_f(const void* x, uint64_t rows, uint64_t cols, uint64_t ld,
                uint8_t* bytes, float* scale, cudaStream_t s) {
   const RowLaunch l = row_launch(rows, cols / W, R);
+  if (l.grid >= (1ull << 31)) return HX_ERR_ARG;
   const T* p = static_cast<const T*>(x);
+  const uint32_t g = (uint32_t)l.grid, c = (uint32_t)cols;
   if (l.twice)
-    k_quantize<T, W, R, true, true><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, bytes, scale);
+    k_quantize<T, W, R, true, true, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, bytes, scale, l.lanes);
   else if (l.block)
-    k_quantize<T, W, R, true, false><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, bytes, scale);
+    k_quantize<T, W, R, true, false, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, bytes, scale, l.lanes);
   else
-    k_quantize<T, W, R, false, false><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, bytes, scale);
+    k_quantize<T, W, R, false, false, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, bytes, scale, l.lanes);
   return launched();
 }
 
-template <typename T, int W, int R>
-int gated_save_w(uint32_t fmt, const void* x, uint64_t rows, uint64_t cols, uint64_t ld, void* out,
+template <typename T, int W, int R, uint32_t F>
+int gated_save_f(const void* x, uint64_t rows, uint64_t cols, uint64_t ld, void* out,
                  uint8_t* bytes, float* scale, cudaStream_t s) {
   const RowLaunch l = row_launch(rows, cols / W, R);
+  if (l.grid >= (1ull << 31)) return HX_ERR_ARG;
   const T* p = static_cast<const T*>(x);
   T* o = static_cast<T*>(out);
+  const uint32_t g = (uint32_t)l.grid, c = (uint32_t)cols;
   if (l.twice)
-    k_gated_save<T, W, R, true, true><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, o, bytes, scale);
+    k_gated_save<T, W, R, true, true, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, o, bytes, scale, l.lanes);
   else if (l.block)
-    k_gated_save<T, W, R, true, false><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, o, bytes, scale);
+    k_gated_save<T, W, R, true, false, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, o, bytes, scale, l.lanes);
   else
-    k_gated_save<T, W, R, false, false><<<l.grid, l.threads, 0, s>>>(fmt, p, rows, (uint32_t)cols, ld, o, bytes, scale);
+    k_gated_save<T, W, R, false, false, F><<<g, l.threads, 0, s>>>(p, rows, c, ld, o, bytes, scale, l.lanes);
   return launched();
 }
 
-uint64_t flat_grid(uint64_t units) { return (units + kFlatThreads - 1) / kFlatThreads; }
+template <typename T, int W, int R, typename... A>
+int quantize_w(uint32_t fmt, A... a) {
+  return fmt == HX_ROWS_E4M3 ? quantize_f<T, W, R, HX_ROWS_E4M3>(a...) : quantize_f<T, W, R, HX_ROWS_INT8>(a...);
+}
+template <typename T, int W, int R, typename... A>
+int gated_save_w(uint32_t fmt, A... a) {
+  return fmt == HX_ROWS_E4M3 ? gated_save_f<T, W, R, HX_ROWS_E4M3>(a...) : gated_save_f<T, W, R, HX_ROWS_INT8>(a...);
+}
+
+// The tasks of rows in units of W, U units per thread, and their grid.
+Tasks tasks_of(uint64_t rows, uint64_t cols, int W, int U, uint64_t* grid) {
+  Tasks t{};
+  const uint64_t units = cols / W;
+  t.rows = rows, t.cols = (uint32_t)cols;
+  t.n = std::min<uint32_t>(32, power_of_two((units + U - 1) / U));
+  for (t.shift = 0; (1u << t.shift) < t.n; ++t.shift) {
+  }
+  t.per_row = (uint32_t)((units + t.n * U - 1) / (t.n * U));
+  *grid = (rows * t.per_row * t.n + kFlatThreads - 1) / kFlatThreads;
+  return t;
+}
 
 // f(T{}) for the element type.
 template <typename F>
@@ -330,6 +394,32 @@ int by_type(uint32_t dtype, F f) {
   if (dtype == HX_F32) return f(float{});
   if (dtype == HX_F16) return f(__half{});
   return f(__nv_bfloat16{});
+}
+
+// f(W, U) as compile-time values for the element type, the unit and the units per thread: 32 bytes' worth (4 of 8 or 4
+// values, 8 of fewer) once they still make four blocks per SM, else one, for as many threads as there are units.
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+template <typename T, int W, typename F>
+int by_count(uint64_t rows, uint64_t cols, F f) {
+  constexpr int kMany = W >= 4 ? 4 : 8;
+  uint64_t grid;
+  Tasks t = tasks_of(rows, cols, W, kMany, &grid);
+  const bool many = grid >= 4 * 148;
+  if (!many) t = tasks_of(rows, cols, W, 1, &grid);
+  if (grid >= (1ull << 31)) return HX_ERR_ARG;
+  return many ? f(Count<W>{}, Count<kMany>{}, t, (uint32_t)grid) : f(Count<W>{}, Count<1>{}, t, (uint32_t)grid);
+}
+template <typename T, typename F>
+int by_unit(int w, uint64_t rows, uint64_t cols, F f) {
+  if constexpr (sizeof(T) == 2) {
+    if (w == 8) return by_count<T, 8>(rows, cols, f);
+  }
+  if (w == 4) return by_count<T, 4>(rows, cols, f);
+  if (w == 2) return by_count<T, 2>(rows, cols, f);
+  return by_count<T, 1>(rows, cols, f);
 }
 
 }  // namespace
@@ -342,12 +432,16 @@ int hx_quantize_rows(uint32_t format, uint32_t dtype, const void* d_x, uint64_t 
   if (!rows) return HX_OK;
   if (!d_x || !d_bytes || !d_scale || !multiple(d_x, size_of(dtype)) || !multiple(d_scale, 4))
     return HX_ERR_ARG;
-  const bool w = wide(dtype, cols, rows > 1 ? ld : cols, d_x, nullptr, d_bytes);
+  const int w = unit_of(dtype, cols, rows > 1 ? ld : cols, d_x, nullptr, d_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return w ? quantize_w<T, 8, 4>(format, d_x, rows, cols, ld, d_bytes, d_scale, s)
-             : quantize_w<T, 1, 8>(format, d_x, rows, cols, ld, d_bytes, d_scale, s);
+    if constexpr (sizeof(T) == 2) {
+      if (w == 8) return quantize_w<T, 8, 4>(format, d_x, rows, cols, ld, d_bytes, d_scale, s);
+    }
+    if (w == 4) return quantize_w<T, 4, 8>(format, d_x, rows, cols, ld, d_bytes, d_scale, s);
+    if (w == 2) return quantize_w<T, 2, 8>(format, d_x, rows, cols, ld, d_bytes, d_scale, s);
+    return quantize_w<T, 1, 16>(format, d_x, rows, cols, ld, d_bytes, d_scale, s);
   });
 }
 
@@ -357,24 +451,15 @@ int hx_dequantize_rows(uint32_t format, uint32_t dtype, const uint8_t* d_bytes, 
   if (!rows) return HX_OK;
   if (!d_out || !d_bytes || !d_scale || !multiple(d_out, size_of(dtype)) || !multiple(d_scale, 4))
     return HX_ERR_ARG;
-  const bool w = wide(dtype, cols, rows > 1 ? ld : cols, d_out, nullptr, d_bytes);
+  const int w = unit_of(dtype, cols, rows > 1 ? ld : cols, d_out, nullptr, d_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    const uint64_t n = rows * (w ? cols / 8 : cols);
-    if (flat_grid(n) >= (1ull << 31)) return (int)HX_ERR_ARG;
-    T* o = static_cast<T*>(d_out);
-    const uint32_t grid = (uint32_t)flat_grid(n), many = (grid + 3) / 4;
-    // four units per thread once that still makes four blocks per SM, as many as a small input can have else
-    if (w && many >= 4 * 148)
-      k_dequantize<T, 8, 4><<<many, kFlatThreads, 0, s>>>(format, d_bytes, d_scale, n, (uint32_t)cols, o, ld);
-    else if (w)
-      k_dequantize<T, 8, 1><<<grid, kFlatThreads, 0, s>>>(format, d_bytes, d_scale, n, (uint32_t)cols, o, ld);
-    else if (many >= 4 * 148)
-      k_dequantize<T, 1, 4><<<many, kFlatThreads, 0, s>>>(format, d_bytes, d_scale, n, (uint32_t)cols, o, ld);
-    else
-      k_dequantize<T, 1, 1><<<grid, kFlatThreads, 0, s>>>(format, d_bytes, d_scale, n, (uint32_t)cols, o, ld);
-    return launched();
+    return by_unit<T>(w, rows, cols, [&](auto W, auto U, const Tasks& k, uint32_t grid) {
+      k_dequantize<T, decltype(W)::value, decltype(U)::value>
+          <<<grid, kFlatThreads, 0, s>>>(format, d_bytes, d_scale, k, static_cast<T*>(d_out), ld);
+      return launched();
+    });
   });
 }
 
@@ -386,22 +471,23 @@ int hx_gated_forward(uint32_t format, uint32_t dtype, const void* d_x, uint64_t 
   if (!d_x || !d_out || !multiple(d_x, size_of(dtype)) || !multiple(d_out, size_of(dtype)) ||
       !multiple(d_scale, 4))
     return HX_ERR_ARG;
-  const bool w = wide(dtype, cols, rows > 1 ? ld : cols, d_x, d_out, d_bytes);
+  const int w = unit_of(dtype, cols, rows > 1 ? ld : cols, d_x, d_out, d_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    if (d_bytes)
-      return w ? gated_save_w<T, 8, 4>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s)
-               : gated_save_w<T, 1, 8>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s);
-    const uint64_t n = rows * (w ? cols / 8 : cols);
-    if (flat_grid(n) >= (1ull << 31)) return (int)HX_ERR_ARG;
-    const T* x = static_cast<const T*>(d_x);
-    T* o = static_cast<T*>(d_out);
-    if (w)
-      k_gated<T, 8><<<(uint32_t)flat_grid(n), kFlatThreads, 0, s>>>(x, n, (uint32_t)cols, ld, o);
-    else
-      k_gated<T, 1><<<(uint32_t)flat_grid(n), kFlatThreads, 0, s>>>(x, n, (uint32_t)cols, ld, o);
-    return launched();
+    if (d_bytes) {
+      if constexpr (sizeof(T) == 2) {
+        if (w == 8) return gated_save_w<T, 8, 4>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s);
+      }
+      if (w == 4) return gated_save_w<T, 4, 4>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s);
+      if (w == 2) return gated_save_w<T, 2, 8>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s);
+      return gated_save_w<T, 1, 8>(format, d_x, rows, cols, ld, d_out, d_bytes, d_scale, s);
+    }
+    return by_unit<T>(w, rows, cols, [&](auto W, auto U, const Tasks& k, uint32_t grid) {
+      k_gated<T, decltype(W)::value, decltype(U)::value>
+          <<<grid, kFlatThreads, 0, s>>>(static_cast<const T*>(d_x), k, ld, static_cast<T*>(d_out));
+      return launched();
+    });
   });
 }
 
@@ -414,19 +500,16 @@ int hx_gated_backward(uint32_t format, uint32_t dtype, const void* d_dout, uint6
   if (!d_dout || !d_bytes || !d_scale || !d_dx || !multiple(d_dout, e) || !multiple(d_dx, e) ||
       !multiple(d_out, e) || !multiple(d_scale, 4))
     return HX_ERR_ARG;
-  const bool w = wide(dtype, cols, rows > 1 ? ld : cols, d_dout, d_dx, d_bytes) && multiple(d_out, 16);
+  int w = unit_of(dtype, cols, rows > 1 ? ld : cols, d_dout, d_dx, d_bytes);
+  while (w > 1 && !multiple(d_out, w * e)) w /= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    const uint64_t n = rows * (w ? cols / 8 : cols);
-    if (flat_grid(n) >= (1ull << 31)) return (int)HX_ERR_ARG;
-    const T* d = static_cast<const T*>(d_dout);
-    T *dx = static_cast<T*>(d_dx), *h = static_cast<T*>(d_out);
-    if (w)
-      k_gated_backward<T, 8><<<(uint32_t)flat_grid(n), kFlatThreads, 0, s>>>(format, d, ld, d_bytes, d_scale, n, (uint32_t)cols, dx, h);
-    else
-      k_gated_backward<T, 1><<<(uint32_t)flat_grid(n), kFlatThreads, 0, s>>>(format, d, ld, d_bytes, d_scale, n, (uint32_t)cols, dx, h);
-    return launched();
+    return by_unit<T>(w, rows, cols, [&](auto W, auto U, const Tasks& k, uint32_t grid) {
+      k_gated_backward<T, decltype(W)::value, decltype(U)::value><<<grid, kFlatThreads, 0, s>>>(
+          format, static_cast<const T*>(d_dout), ld, d_bytes, d_scale, k, static_cast<T*>(d_dx), static_cast<T*>(d_out));
+      return launched();
+    });
   });
 }
 

@@ -107,6 +107,12 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < kRaw; ++i) r[i] = 0;
   }
+  // Keeps what is computed from the values behind this point: without it the compiler may do that work ahead of a
+  // reduction that does not need it, and hold its larger results instead of these registers.
+  __device__ __forceinline__ void pin() {
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) asm volatile("" : "+r"(r[i]));
+  }
   // bits of the largest magnitude so far (as T's bits; NaN and infinities compare above all
   // finite values), per 16-bit half for 16-bit types (the packed maximum keeps a NaN)
   __device__ __forceinline__ uint32_t top(uint32_t m) const {
@@ -228,10 +234,10 @@ __device__ __forceinline__ Scale scale_of(uint32_t fmt, uint32_t bits) {
   return r;
 }
 
-// W values to bytes. INT8 is the nearest integer (ties to even) of the 32-bit quotient x / s. x * inv
-// is within 2^-15 of that quotient (|x / s| <= 128; inv, the product and the quotient each round
-// once, 3 * 2^-24 * 128 < 2^-15), so it rounds to the same integer unless it lies within 2^-14 of
-// a half: then the division itself decides. Adding 1.5 * 2^23 leaves that integer in the low byte.
+// W values to bytes. INT8 is the nearest integer (ties to even) of the 32-bit quotient x / s. Adding 1.5 * 2^23 in one
+// fused step leaves the nearest integer of x * inv in the low byte. x * inv is within 2^-16 of that quotient (|x / s| <= 128; inv
+// and the quotient each round once, 2 * 2^-24 * 128), so both round to the same integer unless x * inv lies within 2^-14 of
+// a half: then the division itself decides. So it does for a scale at its upper bound, under which a value can reach 128.
 template <int W>
 __device__ __forceinline__ Bytes<W> to_bytes(uint32_t fmt, const float (&x)[W], const Scale& sc) {
   Bytes<W> out;
@@ -250,14 +256,14 @@ __device__ __forceinline__ Bytes<W> to_bytes(uint32_t fmt, const float (&x)[W], 
   } else {
     constexpr float kRound = 12582912.0f;
     uint32_t q[W];
-    bool near = false;
+    float off = 0.0f;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const float t = fminf(fmaxf(x[i] * sc.inv, -127.0f), 127.0f);
-      const float r = __fadd_rn(t, kRound);
+      const float r = __fmaf_rn(x[i], sc.inv, kRound);
       q[i] = __float_as_uint(r);
-      near |= fabsf(t - __fsub_rn(r, kRound)) > 0.5f - 0x1p-14f;
+      off = fmaxf(off, fabsf(__fmaf_rn(x[i], sc.inv, -__fsub_rn(r, kRound))));
     }
+    const bool near = off > 0.5f - 0x1p-14f || sc.s >= 0x1p121f;
     if (near) {
 #pragma unroll
       for (int i = 0; i < W; ++i)
