@@ -10,6 +10,7 @@ over the data). The scales, one per row, stay as they are.
     key = store.put(data, scale)             # forward: coded on the current stream
     store.seal()                             # streams trimmed to their size (reads the sizes: one wait)
     data, scale = store.take(key)            # backward: decoded, and forgotten by the store
+    store.check()                            # once per step: raises if a coding or decoding failed
 """
 from __future__ import annotations
 
@@ -28,10 +29,13 @@ class _Entry:
 
 class CheckpointStore:
     """Coded 8-bit rows by key. All calls of a store are made on one CUDA stream. `hist` (int32[256] on the
-    device), if given, accumulates the histogram of all bytes put, for the next codebook."""
+    device), if given, accumulates the histogram of all bytes put, for the next codebook. Errors in the data
+    (a byte without a code, a stream that does not decode) are kept on the device until seal() or check() reads
+    them; what take() gave before that is not to be relied on."""
 
     def __init__(self, tables, kind: int = hx.KIND_HUFFMAN, hist=None):
         self.tables, self.kind, self.hist = tables, kind, hist
+        self._status = hx.new_status(tables.device)
         self._entries: dict[int, _Entry] = {}
         self._next = 0
         self._scratch = None
@@ -77,19 +81,25 @@ class CheckpointStore:
         if failed:
             raise hx.HxError(failed, "CheckpointStore.seal")
 
-    def take(self, key: int, status=None):
-        """Decodes the rows of `key`: (bytes, scale). The store forgets them. Errors in the data go to
-        `status` (a device status word), if given."""
+    def take(self, key: int):
+        """Decodes the rows of `key`: (bytes, scale). The store forgets them."""
         import torch
         e = self._entries.pop(key)
+        if e.status is not None:  # not sealed: what its coding raised is read by check()
+            self._status |= e.status
         n = 1
         for d in e.shape:
             n *= d
         out = torch.empty(max(n, 1), dtype=torch.uint8, device=e.stream.device)[:n]
-        if status is None:
-            status = hx.new_status(e.stream.device)
-        hx.decode(self.tables, e.stream, n, out=out, status=status, kind=self.kind)
+        hx.decode(self.tables, e.stream, n, out=out, status=self._status, kind=self.kind)
         return out.view(e.shape), e.scale
+
+    def check(self) -> None:
+        """Waits for the device and raises HxError if anything taken so far was not coded or decoded exactly."""
+        code = int(self._status.item())
+        if code:
+            self._status.zero_()
+            raise hx.HxError(code, "CheckpointStore.check")
 
     def nbytes(self) -> int:
         """Device bytes of the streams and scales held."""

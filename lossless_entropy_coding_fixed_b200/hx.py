@@ -512,7 +512,8 @@ class Session:
 # --------------------------------------------------------------------------------- 8-bit rows
 # A matrix kept as bytes (uint8, contiguous) and one float32 scale per row (include/hx.h, "8-bit
 # rows"). Every call runs on the tensors' device and that device's current stream, whichever device is
-# current; outputs are allocated unless they are given. A small call's time is its host time, so the
+# current; outputs are allocated unless they are given. The calls are explicit forward and backward passes: they record
+# no autograd graph. A small call's time is its host time, so the
 # checks are plain comparisons and the stream is read as the raw handle.
 _torch = None
 

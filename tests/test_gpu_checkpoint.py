@@ -32,24 +32,24 @@ def tables_for(samples, cuda, kind=hx.KIND_HUFFMAN):
 def test_store_gives_back_every_byte(cuda, kind, fmt):
     g = torch.Generator(device=cuda).manual_seed(4)
     rows = [hx.quantize_rows(0.5 * torch.randn(r, c, generator=g, device=cuda).bfloat16(), fmt)
-            for r, c in ((1, 1), (300, 700), (64, 4096), (777, 1365), (1024, 4096))]
+            for r, c in ((0, 8), (1, 1), (300, 700), (64, 4096), (777, 1365), (1024, 4096))]
     hist = torch.zeros(256, dtype=torch.int32, device=cuda)
     store = CheckpointStore(tables_for([b for b, _ in rows], cuda, kind), kind, hist=hist)
-    keys = [store.put(b, s) for b, s in rows[:3]]
+    keys = [store.put(b, s) for b, s in rows[:4]]
     unsealed = store.nbytes()
     store.seal()
     assert store.nbytes() < unsealed
-    keys += [store.put(b, s) for b, s in rows[3:]]
+    keys += [store.put(b, s) for b, s in rows[4:]]
     raw = sum(b.numel() for b, _ in rows)
     late = store.take(keys.pop())  # not sealed
     assert torch.equal(late[0], rows[-1][0]) and late[1] is rows[-1][1]
     store.seal()
     store.seal()
-    assert store.nbytes() < sum(b.numel() + 4 * s.numel() for b, s in rows[:4])
+    assert store.nbytes() < sum(b.numel() + 4 * s.numel() for b, s in rows[:5])
     for key, (b, s) in reversed(list(zip(keys, rows))):
-        st = hx.new_status(cuda)
-        got, sc = store.take(key, st)
-        assert torch.equal(got, b) and sc is s and int(st.item()) == 0
+        got, sc = store.take(key)
+        assert torch.equal(got, b) and sc is s
+    store.check()
     assert len(store) == 0 and int(hist.sum()) == raw
     with pytest.raises(KeyError):
         store.take(keys[0])
@@ -66,6 +66,13 @@ def test_store_reports_a_byte_without_a_code(cuda):
         store.seal()
     assert e.value.code == hx.HX_ERR_UNCODABLE and len(store) == 1
     assert (store.take(good)[0] == 3).all()
+    store.check()
+    bad = store.put(torch.full((4, 100), 30, dtype=torch.uint8, device=cuda), s)
+    store.take(bad)  # before anything was read back
+    with pytest.raises(hx.HxError) as e:
+        store.check()
+    assert e.value.code & hx.HX_ERR_UNCODABLE
+    store.check()  # told once
     with pytest.raises(TypeError):
         store.put(s, s)
 
