@@ -596,9 +596,12 @@ __global__ void __launch_bounds__(1024) k_qk_weights(const float* __restrict__ p
   float* dw = blockIdx.y ? dwk : dwq;
   if (hi - lo == 1) return;  // written by its one block
   float v = 0.0f;
-  if (d < dim) {
-#pragma unroll 8
-    for (uint32_t b = lo + k; b < hi; b += 32) v += part[(uint64_t)b * dim + d];
+  for (uint32_t b = lo + k; b < hi; b += 256) {  // eight loads at once: one round for the 256 rows a class mostly has
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = d < dim && b + 32 * i < hi ? part[(uint64_t)(b + 32 * i) * dim + d] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += p[i];
   }
   rows[k][x] = v;
   __syncthreads();

@@ -808,7 +808,9 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     ldw = _matrix(out, "out")[2]
     fn = lib()
     yp = dy.data_ptr()
-    need = fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
+    # rows on 16 (dy) and 8 bytes need no workspace
+    need = (fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
+            if (yp | 2 * ld) % 16 or (db | n_in) % 8 else 0)
     ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, _dtype(out),
             out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
