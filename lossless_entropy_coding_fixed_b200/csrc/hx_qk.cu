@@ -560,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
     }
   }
 
+  // (the kernel that adds the blocks' sums may be set up from here on; it waits for this one's end)
+  asm volatile("griddepcontrol.launch_dependents;");
   // the block's sum of its groups' weight gradients, in the groups' order
   float* mine = sums + group * (16 * a.lanes);
 #pragma unroll
@@ -594,6 +596,7 @@ __global__ void __launch_bounds__(1024) k_qk_weights(const float* __restrict__ p
   const uint32_t x = threadIdx.x & 31, k = threadIdx.x >> 5, d = blockIdx.x * 32 + x;
   const uint32_t lo = blockIdx.y ? blocks_q : 0, hi = blockIdx.y ? blocks : blocks_q;
   float* dw = blockIdx.y ? dwk : dwq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (hi - lo == 1) return;  // written by its one block
   float v = 0.0f;
   for (uint32_t b = lo + k; b < hi; b += 256) {  // eight loads at once: one round for the 256 rows a class mostly has
@@ -789,9 +792,20 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
     // a class with one block has its sums; one without heads has none to write
     if (q <= 1 && k <= 1 && (q || !d_dwq) && (k || !d_dwk)) return HX_OK;
   }
-  k_qk_weights<<<dim3((a.dim + 31) / 32, 2), 1024, 0, s>>>(a.part, a.dim, a.blocks_q, (uint32_t)blocks,
-                                                        d_dwq, d_dwk);
-  return launched();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((a.dim + 31) / 32, 2);
+  c.blockDim = dim3(1024);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at, c.numAttrs = a.tokens ? 1 : 0;
+  if (cudaLaunchKernelEx(&c, k_qk_weights, static_cast<const float*>(a.part), a.dim, a.blocks_q, (uint32_t)blocks, d_dwq,
+                         d_dwk) != cudaSuccess) {
+    cudaGetLastError();
+    return HX_ERR_CUDA;
+  }
+  return HX_OK;
 }
 
 }  // extern "C"
