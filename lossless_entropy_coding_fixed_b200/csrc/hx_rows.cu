@@ -13,6 +13,10 @@
 //   k_gated, k_gated_backward, k_dequantize
 //                  the scales are known (or not needed): U units per thread of a group of 1 to 32 lanes, the loads
 //                  of all before the first is used.
+//
+// Measured on B200, 8192 x 8192 values (floor: the bytes at the measured copy rate, 6550 GB/s): f32 to INT8 52 us (51),
+// e4m3 to bf16 33 (31), gated bf16 saved as e4m3 82 (82), its backward pass with h 101 (102). Rows in units of one value
+// (odd widths) take 1.6 to 2.5 times the wide ones' time, in units of two 1.2 to 1.5 times.
 #include <algorithm>
 #include <cstdint>
 

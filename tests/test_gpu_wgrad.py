@@ -78,6 +78,31 @@ def test_against_the_product(cuda, size, dt, fmt):
         check(dw, dy, b, s, dt, fmt, old)
 
 
+@pytest.mark.parametrize("fmt,size", [  # tile and splits of the tokens by the estimate: 128 x 128 ..
+    ("e4m3", (300, 22, 4)), ("int8", (640, 641, 922)), ("int8", (640, 517, 770)), ("e4m3", (640, 1036, 261)),  # 1 2 3 4
+    ("e4m3", (640, 8, 7)), ("e4m3", (1000, 933, 132)), ("e4m3", (3000, 3, 6)),  # 5 6 8
+    ("e4m3", (2000, 772, 1316)), ("e4m3", (3000, 771, 784)), ("int8", (2000, 650, 897))])  # 256 x 256: 2 3 4
+def test_every_number_of_splits(cuda, fmt, size):
+    dy, b, s = setup(*size, "bf16", fmt, cuda, seed=size[1])
+    n, k = size[1:]
+    for out in ("bf16", "f32"):
+        check(hx.weight_grad(dy, b, s, FMT[fmt], dtype=DT[out]), dy, b, s, "bf16", fmt)
+    old = torch.randn(n, k, device=cuda)
+    check(hx.weight_grad(dy, b, s, FMT[fmt], out=old.clone(), accumulate=True), dy, b, s, "bf16", fmt, old)
+
+
+def test_scales_that_are_no_powers_of_two(cuda):
+    """e4m3 rows of a caller's own scales: rounded once in the product, not the scale."""
+    dy, b, s = setup(200, 136, 264, "bf16", "e4m3", cuda, seed=8)
+    s = s * 1.2345
+    table = (ref.values(np.arange(256, dtype=np.uint8)[None], np.ones(1), "e4m3"))[0]
+    table[~np.isfinite(table)] = 0
+    x = (torch.from_numpy(table).to(cuda)[b.long()].float() * s[:, None]).bfloat16().double()
+    want, mags = dy.double().T @ x, dy.double().abs().T @ x.abs()
+    dw = hx.weight_grad(dy, b, s, dtype=torch.float32).double()
+    assert ((dw - want).abs() <= mags * ((200 + 64) * 2.0 ** -23)).all()
+
+
 @pytest.mark.parametrize("T", [40, 3000])
 @pytest.mark.parametrize("pad,shift", [(0, 1), (8, 0), (8, 8), (1, 0), (16, 4)])
 def test_strides_and_alignment(cuda, T, pad, shift):
