@@ -638,23 +638,35 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
   }
 }
 
-// Copies rows to a pitch that TMA and the 8-byte loads take: `chunks` pieces of 8 bytes per row, the last
-// one zero-filled. E: the element (2 or 1 bytes).
+// Copies rows to a pitch that TMA and the 8-byte loads take: `chunks` pieces of 16 bytes per row, what is behind the row's
+// end zero. E: the element (2 or 1 bytes). A piece inside its row is read in five aligned words, which reach up to three
+// bytes into the row before and behind it; where the row does not have those, by its elements.
 template <typename E>
-__device__ __forceinline__ void align_piece(const E* src, uint64_t ld, uint64_t cols, uint64_t* dst, uint32_t chunks, uint64_t i) {
-  constexpr uint32_t kPer = 8 / sizeof(E);
-  const uint64_t row = i / chunks, c = (i - row * chunks) * kPer;
+__device__ __forceinline__ void align_piece(const E* src, uint64_t ld, uint64_t cols, uint4* dst, uint32_t chunks, uint64_t i) {
+  constexpr uint32_t kPer = 16 / sizeof(E);
+  const uint64_t row = i >> 32 ? i / chunks : (uint32_t)i / chunks, c = (i - row * chunks) * kPer;
   const E* p = src + row * ld + c;
-  uint64_t v = 0;
+  uint32_t v[4] = {0, 0, 0, 0};
+  if (c && c + kPer + 4 / sizeof(E) - 1 <= cols) {
+    const uint32_t shift = (reinterpret_cast<uintptr_t>(p) & 3) * 8;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+    uint32_t x[5];
 #pragma unroll
-  for (uint32_t k = 0; k < kPer; ++k)
-    if (c + k < cols) v |= (uint64_t)p[k] << (8 * sizeof(E) * k);
-  dst[i] = v;
+    for (int k = 0; k < 4; ++k) x[k] = w[k];
+    x[4] = shift ? w[4] : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __funnelshift_r(x[k], x[k + 1], shift);
+  } else {
+#pragma unroll
+    for (uint32_t k = 0; k < kPer; ++k)
+      if (c + k < cols) v[k * sizeof(E) / 4] |= (uint32_t)p[k] << (8 * (k * sizeof(E) % 4));
+  }
+  dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
 }
 __global__ void __launch_bounds__(256)
-    k_wgrad_align(const uint16_t* dy, uint64_t ld_dy, uint64_t n_out, uint64_t* dy_out, const uint8_t* x, uint64_t n_in,
-                  uint64_t* x_out, uint64_t tokens, uint32_t dy_blocks) {
-  const uint32_t cy = (uint32_t)((n_out + 7) / 8 * 2), cx = (uint32_t)((n_in + 15) / 16 * 2);
+    k_wgrad_align(const uint16_t* dy, uint64_t ld_dy, uint64_t n_out, uint4* dy_out, const uint8_t* x, uint64_t n_in,
+                  uint4* x_out, uint64_t tokens, uint32_t dy_blocks) {
+  const uint32_t cy = (uint32_t)((n_out + 7) / 8), cx = (uint32_t)((n_in + 15) / 16);
   const bool first = blockIdx.x < dy_blocks;
   const uint64_t all = tokens * (first ? cy : cx), step = (uint64_t)(first ? dy_blocks : gridDim.x - dy_blocks) * 256;
   for (uint64_t i = (uint64_t)(first ? blockIdx.x : blockIdx.x - dy_blocks) * 256 + threadIdx.x; i < all; i += step) {
@@ -814,10 +826,10 @@ int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t l
   uint64_t pitch = tokens > 1 ? ld_dy * 2 : (n_out + 7) / 8 * 16;
   if (need.dy + need.x) {
     uint8_t* w = static_cast<uint8_t*>(d_workspace);
-    const uint64_t by = ceil_div(need.dy / 8, 256), bx = ceil_div(need.x / 8, 256), most = 148 * 16;
+    const uint64_t by = ceil_div(need.dy / 16, 256), bx = ceil_div(need.x / 16, 256), most = 148 * 8;
     const uint32_t gy = (uint32_t)std::min(by, most), gx = (uint32_t)std::min(bx, most);
-    k_wgrad_align<<<gy + gx, 256, 0, s>>>(static_cast<const uint16_t*>(d_dy), ld_dy, n_out, reinterpret_cast<uint64_t*>(w),
-                                          d_bytes, n_in, reinterpret_cast<uint64_t*>(w + need.dy), tokens, gy);
+    k_wgrad_align<<<gy + gx, 256, 0, s>>>(static_cast<const uint16_t*>(d_dy), ld_dy, n_out, reinterpret_cast<uint4*>(w),
+                                          d_bytes, n_in, reinterpret_cast<uint4*>(w + need.dy), tokens, gy);
     if (const int rc = launched()) return rc;
     if (need.dy) dy = w, pitch = (n_out + 7) / 8 * 16;
     if (need.x) a.bytes = w + need.dy, a.ld_x = (n_in + 15) / 16 * 16;
