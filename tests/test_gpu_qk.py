@@ -187,6 +187,39 @@ def test_heads_that_are_not_finite(cuda):
     assert torch.isnan(dx[hit]).all() and torch.isfinite(dx[~hit]).all()
 
 
+def test_more_values_than_32_bits(cuda):
+    """Offsets beyond 2^32 values, in place: a few tokens of a large batch against a small one of the same."""
+    T, H, D = (1 << 17) + 3, 128, 256
+    p = setup(6, 96, 32, D, D, "bf16", cuda, places=64)
+    at = torch.tensor([0, 1, 65536, 131071, 131072, T - 1], device=cuda)
+    want = hx.head_norm_rope_forward(p["x"], *args(p, 96), eps=EPS)
+    back = hx.head_norm_rope_backward(p["dy"], want[1], want[2], *args(p, 96), eps=EPS)
+    x = torch.zeros(T, H, D, dtype=torch.bfloat16, device=cuda)
+    x[at] = p["x"]
+    pos = torch.zeros(T, dtype=torch.int64, device=cuda)
+    pos[at] = p["pos"]
+    big = dict(p, pos=pos)
+    y, b, s = hx.head_norm_rope_forward(x, *args(big, 96), eps=EPS, out=x)
+    assert torch.equal(y[at], want[0]) and torch.equal(b[at], want[1]) and torch.equal(s[at], want[2])
+    assert int(torch.count_nonzero(s != 1)) <= want[2].numel()
+    x.zero_()
+    x[at] = p["dy"]
+    dx, dwq, dwk = hx.head_norm_rope_backward(x, b, s, *args(big, 96), eps=EPS, out=x)
+    assert torch.equal(dx[at], back[0])
+    for got, w in ((dwq, back[1]), (dwk, back[2])):  # the same terms in another order, and zeros
+        assert float((got - w).abs().max()) <= float(w.abs().max()) * 2.0 ** -14
+
+
+def test_gradients_that_are_broadcast(cuda):
+    """dy with strides of zero: one gradient for every head, or for every token."""
+    p = setup(9, 4, 2, 64, 64, "bf16", cuda)
+    _, b, s = hx.head_norm_rope_forward(p["x"], *args(p, 4), eps=EPS)
+    for dy in (p["dy"][:, :1].expand(9, 6, 64), p["dy"][:1].expand(9, 6, 64)):
+        got = hx.head_norm_rope_backward(dy, b, s, *args(p, 4), eps=EPS)
+        want = hx.head_norm_rope_backward(dy.contiguous(), b, s, *args(p, 4), eps=EPS)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
 def test_no_tokens(cuda):
     p = setup(0, 4, 2, 64, 64, "bf16", cuda, places=4)
     y, b, s = hx.head_norm_rope_forward(p["x"], *args(p, 4))

@@ -64,7 +64,7 @@ def check_rows(x, b, s, fmt):
 
 
 SHAPES = [(1, 1), (3, 2), (9, 7), (9, 8), (33, 31), (12, 255), (10, 1000), (9, 1024), (9, 1025), (9, 1032), (9, 4104),
-          (9, 8192), (9, 16384), (9, 16392), (9, 4097), (2, 40001), (2, 40000)]
+          (9, 8192), (9, 16384), (9, 16392), (9, 4097), (2, 40001), (2, 40000), (9, 1002), (9, 4100), (2, 20002), (2, 20004)]
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
@@ -160,7 +160,8 @@ def gated_check(h, g, u, dt):
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("shape", [(1, 1), (9, 8), (5, 33), (9, 256), (3, 1031), (2, 8192), (2, 16392), (2, 20001)])
+@pytest.mark.parametrize("shape", [(1, 1), (9, 8), (5, 33), (9, 256), (3, 1031), (2, 8192), (2, 16392), (2, 20001),
+                                   (5, 1002), (5, 4100), (2, 20002), (2, 20004)])
 def test_gated_forward_and_backward(cuda, shape, dt, fmt):
     rows, cols = shape
     rng = np.random.default_rng(cols)
@@ -187,6 +188,49 @@ def test_gated_forward_and_backward(cuda, shape, dt, fmt):
     terms = np.abs(d * u) * (p + np.abs(g) * p * (1 - p))
     assert (np.abs(got[:, 0] - dg) <= np.abs(dg) * half_step(dt) + terms * (slack + 2.0 ** -22) + SUB[dt] + 1e-36).all()
     assert (np.abs(got[:, 1] - du) <= np.abs(du) * (half_step(dt) + slack) + SUB[dt] + 1e-36).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(70001, 3), (40001, 17), (9001, 34), (9000, 100), (5000, 248), (3001, 1001), (2000, 2050)])
+def test_many_rows(cuda, shape, dt):
+    """Enough rows for several units per thread and several rows per warp, in every width of unit."""
+    rows, cols = shape
+    g = torch.Generator(device=cuda).manual_seed(cols)
+    x = (torch.randn(rows, 2 * cols, generator=g, device=cuda) * 2).to(DT[dt])
+    x[::97] = 0
+    h, b, s = hx.gated_forward(x, hx.ROWS_E4M3)
+    xs = x.double().cpu().numpy().reshape(rows, 2, cols)
+    gated_check(h, xs[:, 0], xs[:, 1], dt)
+    check_rows(x.view(rows, 2, cols), b, s, "e4m3")
+    assert torch.equal(hx.gated_forward(x, save=False)[0], h)
+    v = ref.values(b.cpu().numpy(), s.cpu().numpy(), "e4m3")
+    back = hx.dequantize_rows(b.view(2 * rows, cols), s.view(-1), dtype=torch.float32)
+    assert (back.cpu().numpy().reshape(v.shape) == v).all()
+    q, qs = hx.quantize_rows(x, hx.ROWS_INT8)
+    check_rows(x, q, qs, "int8")
+    dh = torch.randn(rows, cols, generator=g, device=cuda).to(DT[dt])
+    dx, again = hx.gated_backward(dh, b, s, need_h=True)
+    gated_check(again, v[:, 0], v[:, 1], dt)
+    dg, du = ref.gated_grad(v[:, 0], v[:, 1], dh.double().cpu().numpy())
+    got = dx.double().cpu().numpy().reshape(rows, 2, cols)
+    # values of a normal law, |g| < 16: slope and activation within 27 ulp of terms that are at most 1.1 |dh u| and |dh g|
+    d, u = np.abs(dh.double().cpu().numpy()), np.abs(v[:, 1])
+    assert (np.abs(got[:, 0] - dg) <= np.abs(dg) * half_step(dt) + 1.1 * d * u * 2.0 ** -18 + 1e-37).all()
+    assert (np.abs(got[:, 1] - du) <= np.abs(du) * (half_step(dt) + 2.0 ** -18) + 1e-37).all()
+
+
+def test_gated_output_given(cuda):
+    """An output of the caller's on a start that is not aligned; nothing beside it is written."""
+    x = make(11, 2 * 264, "bf16", 6, cuda)
+    want = hx.gated_forward(x)[0]
+    buf = torch.full((11 * 264 + 16,), 5.0, dtype=torch.bfloat16, device=cuda)
+    for off in (0, 1, 2, 8):
+        out = buf[off:off + 11 * 264].view(11, 264)
+        for save in (True, False):
+            got = hx.gated_forward(x, save=save, out=out)[0]
+            assert same_bits([got], [want]) and got.data_ptr() == out.data_ptr()
+            assert (buf[:off] == 5).all() and (buf[off + 11 * 264:] == 5).all()
+            buf.fill_(5)
 
 
 def test_gated_strided_input(cuda):
