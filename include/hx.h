@@ -401,7 +401,8 @@ typedef struct {
 /* d_x and d_y are addressed by a token and a head stride (so a packed projection is read in
  * place); d_y may be d_x with the same strides. d_bytes (tokens x heads x dim) and d_scale
  * (f32[tokens][heads]): the rows of x; both NULL: nothing is saved. A position outside the tables
- * raises HX_ERR_ARG in *d_status (NULL: not reported) and makes that token's outputs NaN. */
+ * raises HX_ERR_ARG in *d_status (NULL: not reported) and makes that token's outputs NaN. The
+ * outputs of a head with a NaN are NaN, of one with an infinity NaN or 0. */
 int hx_head_norm_rope_forward(const hx_head_norm_rope* p, const void* d_x, uint64_t x_token,
                               uint64_t x_head, void* d_y, uint64_t y_token, uint64_t y_head,
                               uint8_t* d_bytes, float* d_scale, uint32_t* d_status, void* stream);

@@ -73,8 +73,7 @@ struct Units {
   }
 };
 
-// A lane's 16 values as 8 slots of two. Vectors of 2 or more: slots
-// are neighbours, first those of vector 0, then those of vector 1; vectors of 1: slot j is unit j's (a, b).
+// A lane's 16 values as 8 slots of two. Vectors of 2 or more: slots are neighbours, first those of vector 0, then those of vector 1; vectors of 1: slot j is unit j's (a, b).
 // The other value of a pair is in the same slot (kSwap) or in the same place of the other vector.
 template <int PU, bool kInter>
 struct Slots {
@@ -82,7 +81,6 @@ struct Slots {
   static constexpr bool kSwap = kInter || PU == 1;
   // the slot that holds the pairs' other values, to be swapped if kSwap
   static constexpr __device__ int other(int k) { return kSwap ? k : k % PU < H ? k + H : k - H; }
-  static constexpr __device__ bool second(int k) { return !kSwap && k % PU >= H; }
 };
 
 // (Two scalar operations: the packed ones save nothing forward, 45.1 against 45.9 us, and cost moves to register pairs
