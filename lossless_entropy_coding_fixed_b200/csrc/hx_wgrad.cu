@@ -257,9 +257,10 @@ __device__ __forceinline__ void convert(const Bytes<8>& b, float s, uint4 (&out)
   }
 }
 
-// The same for e4m3 in bf16 and a scale that bf16 holds (twice in s2; every scale of the library's): e4m3's values are
-// exact in bf16, so one packed product there rounds as the 32-bit product would.
-__device__ __forceinline__ uint4 convert_bf16(const Bytes<8>& b, uint32_t s2) {
+// The same for e4m3 and a scale that T holds (twice in s2; in bf16 every scale of the library's, in f16 those within its range):
+// e4m3's values are exact in T, so one packed product there rounds as the 32-bit product would.
+template <typename T>
+__device__ __forceinline__ uint4 convert_packed(const Bytes<8>& b, uint32_t s2) {
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -267,10 +268,19 @@ __device__ __forceinline__ uint4 convert_bf16(const Bytes<8>& b, uint32_t s2) {
     asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
         : "=r"(h0), "=r"(h1)
         : "r"(b.b[i]));
-    const float2 v0 = unpack2<__half>(h0), v1 = unpack2<__half>(h1);
-    const uint32_t w0 = pack2<__nv_bfloat16>(v0.x, v0.y), w1 = pack2<__nv_bfloat16>(v1.x, v1.y);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(w0), "r"(s2));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i + 1]) : "r"(w1), "r"(s2));
+    if constexpr (Type<T>::kInf == 0x7f80u) {
+      const float2 v0 = unpack2<__half>(h0), v1 = unpack2<__half>(h1);
+      const uint32_t w0 = pack2<__nv_bfloat16>(v0.x, v0.y), w1 = pack2<__nv_bfloat16>(v1.x, v1.y);
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(w0), "r"(s2));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i + 1]) : "r"(w1), "r"(s2));
+    } else {  // within +-65504; a NaN stays
+      asm("{\n .reg .b32 t;\n mul.rn.f16x2 t, %1, %2;\n min.NaN.f16x2 t, t, %3;\n max.NaN.f16x2 %0, t, %4;\n}"
+          : "=r"(r[2 * i])
+          : "r"(h0), "r"(s2), "r"(0x7bff7bffu), "r"(0xfbfffbffu));
+      asm("{\n .reg .b32 t;\n mul.rn.f16x2 t, %1, %2;\n min.NaN.f16x2 t, t, %3;\n max.NaN.f16x2 %0, t, %4;\n}"
+          : "=r"(r[2 * i + 1])
+          : "r"(h1), "r"(s2), "r"(0x7bff7bffu), "r"(0xfbfffbffu));
+    }
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
@@ -494,12 +504,12 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
           if (t + 2 * j + odd >= a.tokens) b[j].b[0] = b[j].b[1] = 0;
         if (t + (lane & (kTokens - 1)) >= a.tokens) sc = 0.0f;
       }
-      const uint32_t bits = __float_as_uint(sc);
-      if (kParts == 1 && Type<T>::kInf == 0x7f80u && __all_sync(0xffffffffu, (bits & 0xffffu) == 0)) {
-        const uint32_t s2 = bits | bits >> 16;
+      const T narrow = Type<T>::from_f(sc);
+      const uint32_t bits = *reinterpret_cast<const uint16_t*>(&narrow), s2 = bits | bits << 16;
+      if (kParts == 1 && __all_sync(0xffffffffu, Type<T>::to_f(narrow) == sc)) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-          put(B + j * 256 + (swap ^ ((2 * j & 7) << 4)), convert_bf16(b[j], __shfl_sync(0xffffffffu, s2, 2 * j + odd)));
+          put(B + j * 256 + (swap ^ ((2 * j & 7) << 4)), convert_packed<T>(b[j], __shfl_sync(0xffffffffu, s2, 2 * j + odd)));
       } else {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {

@@ -165,6 +165,22 @@ def test_f16_rows_beyond_its_range(cuda):
         assert torch.isfinite(dw).all() and torch.allclose(dw, want.expand(8, 4), rtol=2.0 ** -20, atol=0)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_rows_of_every_level(cuda, dt, fmt):
+    """Scales from far below f16's range to its top, some rows of each in every step of 64 tokens."""
+    T, n, k = 150, 70, 96
+    g = torch.Generator(device=cuda).manual_seed(2)
+    x = torch.randn(T, k, generator=g, device=cuda) * torch.exp2(torch.arange(T, device=cuda) % 37 - 24.0)[:, None]
+    dy = torch.randn(T, n, generator=g, device=cuda).to(DT[dt])
+    b, s = hx.quantize_rows(x, FMT[fmt])
+    check(hx.weight_grad(dy, b, s, FMT[fmt], dtype=torch.float32), dy, b, s, dt, fmt)
+    for lo, hi in ((0, 13), (24, 37)):  # of one kind only: the smallest, the largest
+        rows = ((torch.arange(T, device=cuda) % 37 >= lo) & (torch.arange(T, device=cuda) % 37 < hi)).nonzero()[:, 0]
+        part = [t[rows].contiguous() for t in (dy, b, s)]
+        check(hx.weight_grad(*part, FMT[fmt], dtype=torch.float32), *part, dt, fmt)
+
+
 @pytest.mark.parametrize("size", [(3000, 256, 256), (600, 515, 70), (100, 3328, 3200)])
 def test_repeated_captured_and_two_at_once(cuda, size):
     """The same bits every time: eager, replayed, and two graphs at once with workspaces of their own."""
