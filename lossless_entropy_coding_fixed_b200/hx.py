@@ -629,9 +629,11 @@ def dequantize_rows(data, scale, fmt: int = ROWS_E4M3, dtype=None, out=None):
     sp = _dense(scale, "scale", shape[:1], torch.float32, dev)
     if out is None:
         out = torch.empty(*shape, dtype=dtype or torch.bfloat16, device=data.device)
+        rows, cols = shape
+        ld = cols
     else:
         _same(out, "out", shape, dtype or out.dtype, dev)
-    rows, cols, ld = _matrix(out, "out")
+        rows, cols, ld = _matrix(out, "out")
     _launch(dev, "hx_dequantize_rows", lib().hx_dequantize_rows, fmt, _dtype(out), db, sp, rows, cols, out.data_ptr(), ld)
     return out
 
@@ -794,24 +796,26 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     dt = _dtype(dy)
     tokens, n_out, ld = _matrix(dy, "dy")
     _device(data, "bytes")
-    if data.dim() != 2:
+    shape = data.shape
+    if len(shape) != 2:
         raise ValueError("bytes must be [tokens, n_in]")
-    n_in = data.shape[1]
+    n_in = shape[1]
     db = _dense(data, "bytes", (tokens, n_in), torch.uint8, dev)
     sp = _dense(scale, "scale", (tokens,), torch.float32, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty(n_out, n_in, dtype=dtype or dy.dtype, device=dy.device)
+        ldw, wt = n_in, dt if dtype is None else _dtype(out)
     else:
         _same(out, "out", (n_out, n_in), dtype or out.dtype, dev)
-    ldw = _matrix(out, "out")[2]
+        ldw, wt = _matrix(out, "out")[2], _dtype(out)
     fn = lib()
     yp = dy.data_ptr()
     # rows on 16 (dy) and 8 bytes need no workspace
     need = (fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
             if (yp | 2 * ld) % 16 or (db | n_in) % 8 else 0)
     ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
-    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, _dtype(out),
+    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, wt,
             out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
     return out
