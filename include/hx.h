@@ -382,7 +382,8 @@ int hx_gated_backward(uint32_t format, uint32_t dtype, const void* d_dout, uint6
  *   k_heads behind them;  y = n with the pairs of its first rot_dim values turned by the angles in
  *   row d_positions[t] of d_cos and d_sin: (a, b) -> (a cos - b sin, b cos + a sin). Pair i is
  *   (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.
- * dim: even, 2..512; rot_dim: even, 0..dim. */
+ * dim: even, 2..512; rot_dim: even, 0..dim. The sum of x^2 is held in 32 bits: a head for which it passes them
+ * (values from 2^64 / sqrt(dim) on) is saved as any other, but its y and dx are 0 or NaN. */
 typedef struct {
   uint32_t format;         /* HX_ROWS_*                                                       */
   uint32_t dtype;          /* of x and y (dy and dx)                                          */

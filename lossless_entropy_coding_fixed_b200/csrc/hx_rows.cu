@@ -87,9 +87,10 @@ __global__ void __launch_bounds__(512)
       if (kLong) v[r].load(xr + (uint64_t)u * W);
       float f[W];
       v[r].floats(f);
-      to_bytes<W>(fmt, f, sc).store(br + (uint64_t)u * W);
+      to_bytes<T, W, false>(fmt, f, sc).store(br + (uint64_t)u * W);
     }
   }
+  if (fmt == HX_ROWS_INT8 && huge<T>(sc)) huge_row<T, W>(xr, br, units, lane, n, sc);
 }
 
 // ----------------------------------------------------------------------------- gated forward
@@ -104,7 +105,7 @@ __device__ __forceinline__ void gate(const float (&g)[W], const float (&u)[W], f
 }
 
 template <typename T, int W, int R, bool kBlock, bool kLong, uint32_t fmt>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1)
     k_gated_save(const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
                  T* __restrict__ out, uint8_t* __restrict__ bytes, float* __restrict__ scale, uint32_t lanes) {
   const uint32_t n = kBlock ? blockDim.x : lanes;
@@ -154,9 +155,13 @@ __global__ void __launch_bounds__(512)
       u[r].floats(fu);
       gate(fg, fu, h);
       store<T, W>(hr + (uint64_t)i * W, h);
-      to_bytes<W>(fmt, fg, sg).store(bg + (uint64_t)i * W);
-      to_bytes<W>(fmt, fu, su).store(bu + (uint64_t)i * W);
+      to_bytes<T, W, false>(fmt, fg, sg).store(bg + (uint64_t)i * W);
+      to_bytes<T, W, false>(fmt, fu, su).store(bu + (uint64_t)i * W);
     }
+  }
+  if (fmt == HX_ROWS_INT8) {
+    if (huge<T>(sg)) huge_row<T, W>(gr, bg, units, lane, n, sg);
+    if (huge<T>(su)) huge_row<T, W>(ur, bu, units, lane, n, su);
   }
 }
 

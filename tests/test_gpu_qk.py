@@ -187,6 +187,26 @@ def test_heads_that_are_not_finite(cuda):
     assert torch.isnan(dx[hit]).all() and torch.isfinite(dx[~hit]).all()
 
 
+@pytest.mark.parametrize("fmt", [hx.ROWS_E4M3, hx.ROWS_INT8])
+@pytest.mark.parametrize("D,inter", [(128, False), (128, True), (48, False), (6, True), (2, False)])
+def test_saved_heads_of_every_level(cuda, D, inter, fmt):
+    """The bytes and scales of a head are the row's, up to bf16's largest values, also when the outputs go where the
+    heads were."""
+    p = setup(40, 4, 2, D, D, "bf16", cuda, seed=D)
+    level = torch.tensor([2.0 ** e for e in (-120, -60, 0, 61, 69, 70, 71, 72, 100, 126)], device=cuda)
+    p["x"] = (p["x"].float().clamp(-1, 1) * level.repeat(4)[:, None, None]).bfloat16()
+    p["x"][:, :, 0] = p["x"][:, :, 0].sign() * (level.repeat(4)[:, None] * 1.5).bfloat16()
+    p["x"][9, 3, 0] = torch.finfo(torch.bfloat16).max
+    want = hx.quantize_rows(p["x"].reshape(-1, D), fmt)
+    y, b, s = hx.head_norm_rope_forward(p["x"], *args(p, 4), eps=EPS, interleaved=inter, fmt=fmt)
+    assert torch.equal(b.reshape(-1, D), want[0]) and torch.equal(s.reshape(-1), want[1].reshape(-1))
+    x = p["x"].clone()
+    y2, b, s = hx.head_norm_rope_forward(x, *args(p, 4), eps=EPS, interleaved=inter, fmt=fmt, out=x)
+    assert torch.equal(b.reshape(-1, D), want[0]) and torch.equal(s.reshape(-1), want[1].reshape(-1))
+    small = level.repeat(4) < 2.0 ** 60
+    assert torch.equal(y2[small], y[small]) and torch.isfinite(y[small]).all()
+
+
 def test_more_values_than_32_bits(cuda):
     """Offsets beyond 2^32 values, in place: a few tokens of a large batch against a small one of the same."""
     T, H, D = (1 << 17) + 3, 128, 256

@@ -151,6 +151,20 @@ def test_int8_ties_and_neighbours(cuda):
     check_rows(x, b, sc, "int8")
 
 
+@pytest.mark.parametrize("dt, e", [("f16", 0), ("f16", -13)] + [("bf16", e) for e in (-124, -110, 0, 69, 70, 71, 72, 73, 127)])
+def test_int8_every_pair_of_a_16_bit_type(cuda, dt, e):
+    """Every significand of a value under every significand of the row's largest, at the nine exponents that reach half
+    a step: the bytes are the 32-bit division's. Scales from 2^-126 on, around 2^64, and up to 2^121."""
+    n = 128 if dt == "bf16" else 1024
+    m = torch.arange(n, 2 * n, dtype=torch.float64) / n
+    x = torch.cat([torch.ldexp(m, torch.tensor(-k)) for k in range(9)])[None].repeat(n, 1)
+    x[:, 1::2] *= -1
+    x[x.abs() > m[:, None]] = 0
+    x = (torch.cat([m[:, None], x], 1) * 2.0 ** e).to(DT[dt])
+    b, s = hx.quantize_rows(x.to(cuda), hx.ROWS_INT8)
+    check_rows(x, b, s, "int8")
+
+
 def gated_check(h, g, u, dt):
     want = ref.gated(g, u)
     tol = np.abs(want) * (half_step(dt) + 2.0 ** -23 * (1.173 * np.abs(g) + 8)) + SUB[dt] + 1e-36 * np.abs(u)
