@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       __syncwarp();
       if (++s == S::kStages) s = 0, parity ^= 1;
     }
-    // the products issued so far end before the TMEM is freed, also when a wait ran out
-    if (elected()) commit<kPair>(done, first);
+    // the products issued so far end before the TMEM is freed, also when a wait ran out. (Without steps nobody waits for
+    // `done`: an arrival in the pair's other CTA could then come after that CTA's end.)
+    if (steps && elected()) commit<kPair>(done, first);
     if (!ok && lane == 0) {
       const uint64_t t0 = now_ns();
       while (!bar_try(done, 0) && now_ns() - t0 < kWaitNs) {

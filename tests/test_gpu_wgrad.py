@@ -135,6 +135,21 @@ def test_no_tokens(cuda):
     assert torch.equal(hx.weight_grad(dy, b, s, out=old.clone(), accumulate=True), old)
 
 
+@pytest.mark.parametrize("n,k", [(1664, 1664), (4096, 4096)])  # pairs of CTAs: 256 x 256, 512 x 256
+def test_no_tokens_of_a_large_product(cuda, n, k):
+    dy = torch.empty(0, n, dtype=torch.bfloat16, device=cuda)
+    b, s = torch.empty(0, k, dtype=torch.uint8, device=cuda), torch.empty(0, device=cuda)
+    for fmt in FMT.values():
+        for dt in ("bf16", "f32"):
+            out = torch.full((n, k), 3.0, dtype=DT[dt], device=cuda)
+            st = hx.new_status(cuda)
+            for _ in range(20):
+                hx.weight_grad(dy, b, s, fmt, out=out, status=st)
+            assert (out == 0).all() and int(st.item()) == 0
+            out.fill_(3)
+            assert (hx.weight_grad(dy, b, s, fmt, out=out, accumulate=True) == 3).all()
+
+
 def test_rows_and_columns_of_the_product(cuda):
     """Each byte's place: one token at a time, one output feature, counted values."""
     T, n, k = 130, 300, 520
