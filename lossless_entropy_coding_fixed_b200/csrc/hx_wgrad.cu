@@ -591,6 +591,10 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
                 : "memory");
         }
       }
+      // The last stages' releases: the first CTA of a pair sends them to the second too, where nothing else waits for them.
+      if (k == steps)
+        for (uint32_t i = k; i < k + S::kStages; ++i)
+          if (!bar_wait(empty(i % S::kStages), ((i / S::kStages) & 1) ^ 1, failed)) break;
       if (k < steps && rank == 0) {  // gave up: wait for the copies already on their way (a pair's, for both)
         const uint64_t t0 = now_ns();
         for (uint32_t i = k > S::kStages ? k - S::kStages : 0; i < k; ++i)

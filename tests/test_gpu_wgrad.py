@@ -215,6 +215,19 @@ def test_repeated_captured_and_two_at_once(cuda, size):
     assert all(torch.equal(h, want) for h in held) and torch.equal(hx.weight_grad(dy, b, s, hx.ROWS_INT8), want)
 
 
+def test_launches_back_to_back(cuda):
+    """Pairs of CTAs of several shapes one right after another, each where another one's has just ended: the same bits."""
+    cases = []
+    for T, n, k in ((65, 1664, 1664), (200, 1664, 1664), (3000, 771, 784), (64, 4096, 4096), (700, 2048, 2048)):
+        dy, b, s = setup(T, n, k, "bf16", "e4m3", cuda, seed=T)
+        cases.append((dy, b, s, hx.weight_grad(dy, b, s), torch.zeros(n, k, dtype=torch.bfloat16, device=cuda)))
+    st = hx.new_status(cuda)
+    for _ in range(30):
+        for dy, b, s, _, out in cases:
+            hx.weight_grad(dy, b, s, out=out, status=st)
+    assert int(st.item()) == 0 and all(torch.equal(out, want) for *_, want, out in cases)
+
+
 def test_status_stays_clear(cuda):
     dy, b, s = setup(300, 200, 100, "bf16", "e4m3", cuda)
     st = hx.new_status(cuda)
