@@ -427,14 +427,23 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
  * An X beyond f16's range counts as +-65504 with HX_F16. d_workspace:
  * hx_weight_grad_workspace() bytes (0: may be NULL), 16-byte aligned, clobbered; needed for rows of dY that do not
  * start on 16 bytes, or of X on 8, which are copied first.
- * Waits inside the kernel are bounded: HX_ERR_TIMEOUT in *d_status (NULL: not reported). tokens = 0: zeros
- * (or the old values). n_out <= 2^23, n_in <= 2^22. */
+ * Waits inside the kernel are bounded (2 s): when one runs out, that part of d_dw is NaN, and HX_ERR_TIMEOUT is raised in
+ * *d_status (NULL: the NaN alone tell). tokens = 0: zeros (or the old values). n_out <= 2^23, n_in <= 2^22. */
 uint64_t hx_weight_grad_workspace(const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes, uint64_t tokens,
                                   uint64_t n_out, uint64_t n_in);
 int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy,
                    const uint8_t* d_bytes, const float* d_scale, uint64_t tokens, uint64_t n_out,
                    uint64_t n_in, uint32_t dw_dtype, void* d_dw, uint64_t ld_dw, int accumulate,
                    void* d_workspace, uint64_t workspace_bytes, uint32_t* d_status, void* stream);
+
+/* hx_weight_grad with its bounded waits exposed, for failure-detection tests: each wait's limit in nanoseconds, and a CTA
+ * (block of the launch) whose part of X never counts as ready (UINT64_MAX, or no such block: none), so that the waits for it
+ * run out. */
+int hx_weight_grad_bounded(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy,
+                           const uint8_t* d_bytes, const float* d_scale, uint64_t tokens, uint64_t n_out,
+                           uint64_t n_in, uint32_t dw_dtype, void* d_dw, uint64_t ld_dw, int accumulate,
+                           void* d_workspace, uint64_t workspace_bytes, uint32_t* d_status, uint64_t wait_ns,
+                           uint64_t withhold, void* stream);
 
 /* Measurement helpers (host, fp64). Shannon entropy -sum p log2 p of counts[256] in bits per
  * symbol ("Single-Stage Huffman Encoder for ML Compression", abstract: the ideal the fixed code

@@ -25,7 +25,8 @@
 // at once, no fence wider than the CTA's own shared memory, whole-line stores.
 //
 // Every wait is bounded (2 s); when one runs out the CTA raises HX_ERR_TIMEOUT, waits for its own
-// copies in flight, frees its TMEM and returns.
+// copies in flight, frees its TMEM and returns. Its cluster's part of the result is NaN then: whatever sums it has are
+// not whole.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -56,6 +57,7 @@ struct Args {
   uint32_t dw_dtype, accumulate, dw_wide;
   uint32_t splits, steps;
   uint32_t* status;
+  uint64_t wait_ns, withhold;  // a wait's limit; a CTA whose converting warps never arrive (tests)
 };
 
 // ------------------------------------------------------------------------------------ barriers
@@ -108,20 +110,20 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 // Waits for the phase of `parity` to complete. False once this wait, or any other of the CTA, ran out.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed, uint64_t limit) {
   const uint64_t t0 = now_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
       if (bar_try(bar, parity)) return true;
     if (*failed) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (now_ns() - t0 > limit) {
       *failed = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
-  return bar_try(bar, parity) || bar_wait_long(bar, parity, failed);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* failed, uint64_t limit) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, failed, limit);
 }
 
 // --------------------------------------------------------------------------------- tensor core
@@ -408,6 +410,17 @@ __device__ __forceinline__ void join_rows(const Args& a, uint32_t tiles, uint32_
   }
 }
 
+// NaN to rows y0 .. y1 - 1 of each of the CTA's MT accumulators (rows m0 + i * M ..).
+template <typename O, int MT, uint32_t M, uint32_t N>
+__device__ __noinline__ void lose_rows(const Args& a, uint32_t m0, uint32_t n0, uint32_t y0, uint32_t y1) {
+  const O nan = Type<O>::from_f(__uint_as_float(0x7fc00000u));
+  for (uint32_t i = threadIdx.x; i < MT * (y1 - y0) * N; i += blockDim.x) {
+    const uint32_t y = i / N, mt = y / (y1 - y0);
+    const uint32_t row = m0 + mt * M + y0 + y % (y1 - y0), col = n0 + i % N;
+    if (row < a.n_out && col < a.n_in) static_cast<O*>(a.dw)[(uint64_t)row * a.ld_dw + col] = nan;
+  }
+}
+
 template <typename T, int MT, bool kPair, int kParts>
 __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a) {
@@ -489,11 +502,12 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       }
     };
     if (group < steps) fetch(group);
+    const bool tells = lane == 0 && blockIdx.x != a.withhold;
     bool ok = true;
     for (uint32_t k = group; k < steps; k += kGroups) {
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
-      if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)))) break;
+      if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed, a.wait_ns)))) break;
       // line line0 + 2 j + odd, its chunks exchanged by the line's place in its eight
       const uint32_t B = tiles + s * S::kStage + S::kA + (ch >> 3) * 8192 + (line0 + odd) * 128;
       const uint32_t swap = ((ch ^ odd) & 7) << 4;
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
+      if (tells) {
         if constexpr (kPair)
           bar_arrive_at(converted(s), first);
         else
@@ -530,7 +544,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       if (k + kGroups < steps) fetch(k + kGroups);
     }
     // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
-    if (ok && steps) ok = bar_wait(done, 0, failed);
+    if (ok && steps) ok = bar_wait(done, 0, failed, a.wait_ns);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (__all_sync(0xffffffffu, ok)) {
       // a block of columns at a time, the warps of a lane quarter in turn; the stages are free by now
@@ -569,7 +583,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       uint32_t k = 0;
       for (; k < steps; ++k) {
         const uint32_t s = k % S::kStages;
-        if (!bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed)) break;
+        if (!bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed, a.wait_ns)) break;
         const int32_t t = (int32_t)((k0 + k) * kStep);
         if constexpr (kPair) {
           // both CTAs' copies count on the first one's barrier
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       // The last stages' releases: the first CTA of a pair sends them to the second too, where nothing else waits for them.
       if (k == steps)
         for (uint32_t i = k; i < k + S::kStages; ++i)
-          if (!bar_wait(empty(i % S::kStages), ((i / S::kStages) & 1) ^ 1, failed)) break;
+          if (!bar_wait(empty(i % S::kStages), ((i / S::kStages) & 1) ^ 1, failed, a.wait_ns)) break;
       if (k < steps && rank == 0) {  // gave up: wait for the copies already on their way (a pair's, for both)
         const uint64_t t0 = now_ns();
         for (uint32_t i = k > S::kStages ? k - S::kStages : 0; i < k; ++i)
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     const uint32_t a0 = operand(tiles), b0 = operand(tiles + S::kA);
     uint32_t s = 0, parity = 0;
     for (uint32_t k = 0; k < steps; ++k) {
-      ok = bar_wait(converted(s), parity, failed) && bar_wait(copied(s), parity, failed);
+      ok = bar_wait(converted(s), parity, failed, a.wait_ns) && bar_wait(copied(s), parity, failed, a.wait_ns);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t at = s * (S::kStage >> 4);
@@ -631,11 +645,22 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       }
     }
   }
+  // a CTA that gave up tells its whole cluster: before the cluster's barrier, so that all know it after
+  __syncwarp();
+  if (*failed && lane < S::kCtas * a.splits)
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(smem_addr(&bars.failed), lane)), "r"(1) : "memory");
   __syncwarp();
   cluster_sync();
-  if (MT == 1 && a.splits > 1) {
+  const bool lost = *failed, joined = MT == 1 && a.splits > 1;
+  const uint32_t y0 = joined ? split * 128 / a.splits : 0, y1 = joined ? (split + 1) * 128 / a.splits : 128;
+  if (lost) {
+    if (a.dw_dtype == HX_F32)
+      lose_rows<float, MT, S::M, S::N>(a, m0, n0, y0, y1);
+    else
+      lose_rows<T, MT, S::M, S::N>(a, m0, n0, y0, y1);
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
+  } else if (joined) {
     // this split's share of the rows: the splits' sums in their order, four columns per thread
-    const uint32_t y0 = split * 128 / a.splits, y1 = (split + 1) * 128 / a.splits;
     if (a.dw_dtype == HX_F32)
       join_rows<float, S::N>(a, tiles, rank, S::kCtas, m0, n0, y0, y1);
     else
@@ -643,7 +668,6 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     __syncwarp();
     cluster_sync();  // a CTA's sums stay until every other one has read them
   }
-  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
   if (warp == kWarps + 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if constexpr (kPair)
@@ -815,10 +839,10 @@ uint64_t hx_weight_grad_workspace(const void* d_dy, uint64_t ld_dy, const uint8_
   return c.dy + c.x;
 }
 
-int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes,
-                   const float* d_scale, uint64_t tokens, uint64_t n_out, uint64_t n_in, uint32_t dw_dtype,
-                   void* d_dw, uint64_t ld_dw, int accumulate, void* d_workspace, uint64_t workspace_bytes,
-                   uint32_t* d_status, void* stream) {
+int hx_weight_grad_bounded(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes,
+                           const float* d_scale, uint64_t tokens, uint64_t n_out, uint64_t n_in, uint32_t dw_dtype,
+                           void* d_dw, uint64_t ld_dw, int accumulate, void* d_workspace, uint64_t workspace_bytes,
+                           uint32_t* d_status, uint64_t wait_ns, uint64_t withhold, void* stream) {
   if (format > HX_ROWS_INT8 || (dtype != HX_F16 && dtype != HX_BF16) || (dw_dtype != HX_F32 && dw_dtype != dtype))
     return HX_ERR_ARG;
   if (bad_sizes(tokens, n_out, n_in) || (tokens > 1 && ld_dy < n_out) || (n_out > 1 && ld_dw < n_in)) return HX_ERR_ARG;
@@ -837,6 +861,7 @@ int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t l
   a.dw = d_dw, a.ld_dw = ld_dw, a.dw_dtype = dw_dtype, a.accumulate = accumulate != 0;
   a.dw_wide = multiple(d_dw, 16) && (n_out == 1 || ld_dw * (dw_dtype == HX_F32 ? 4 : 2) % 16 == 0);
   a.splits = p.splits, a.steps = (uint32_t)ceil_div(tokens, kStep), a.status = d_status;
+  a.wait_ns = wait_ns, a.withhold = withhold;
   const void* dy = d_dy;
   uint64_t pitch = tokens > 1 ? ld_dy * 2 : (n_out + 7) / 8 * 16;
   if (need.dy + need.x) {
@@ -862,6 +887,14 @@ int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t l
       return HX_ERR_CUDA;
   }
   return dtype == HX_F16 ? run<__half>(p, map, a, s) : run<__nv_bfloat16>(p, map, a, s);
+}
+
+int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes,
+                   const float* d_scale, uint64_t tokens, uint64_t n_out, uint64_t n_in, uint32_t dw_dtype,
+                   void* d_dw, uint64_t ld_dw, int accumulate, void* d_workspace, uint64_t workspace_bytes,
+                   uint32_t* d_status, void* stream) {
+  return hx_weight_grad_bounded(format, dtype, d_dy, ld_dy, d_bytes, d_scale, tokens, n_out, n_in, dw_dtype, d_dw, ld_dw,
+                                accumulate, d_workspace, workspace_bytes, d_status, kWaitNs, ~0ull, stream);
 }
 
 }  // extern "C"

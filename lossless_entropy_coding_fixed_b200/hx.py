@@ -109,6 +109,7 @@ def lib():
                                                  u64, P, P, P, u64, P, P]),
             "hx_weight_grad_workspace": (u64, [P, u64, P, u64, u64, u64]),
             "hx_weight_grad": (i32, [u32, u32, P, u64, P, P, u64, u64, u64, u32, P, u64, i32, P, u64, P, P]),
+            "hx_weight_grad_bounded": (i32, [u32, u32, P, u64, P, P, u64, u64, u64, u32, P, u64, i32, P, u64, P, u64, u64, P]),
             "hx_entropy": (ctypes.c_double, [P]),
             "hx_mean_length": (ctypes.c_double, [P, CB]),
             "hx_version": (i32, []),
@@ -790,7 +791,21 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
                 status=None):
     """hx_weight_grad: dY^T X [n_out, n_in] of a linear layer, from dy [tokens, n_out] (float16 or bfloat16) and the
     8-bit rows of its input X [tokens, n_in]. The result has `dtype` (dy's, or float32), or goes to the
-    matrix `out`, onto its old values if `accumulate`."""
+    matrix `out`, onto its old values if `accumulate`. If a wait inside the kernel runs out (2 s; it does not, on a sound
+    GPU), that part of the result is NaN, and HX_ERR_TIMEOUT is raised in `status`, if given."""
+    return _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status)
+
+
+def weight_grad_bounded(dy, data, scale, wait_ns: int, withhold: int = (1 << 64) - 1, fmt: int = ROWS_E4M3, out=None,
+                        dtype=None, accumulate: bool = False, status=None):
+    """hx_weight_grad_bounded: weight_grad() with its waits' limit in nanoseconds and, for failure tests, a block of the
+    launch (`withhold`) whose part never counts as ready. Returns (result, status)."""
+    if status is None:
+        status = new_status(dy.device)
+    return _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status, (wait_ns, withhold)), status
+
+
+def _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status, bounded=()):
     torch = _torch or _load_torch()
     dev = _device(dy, "dy")
     dt = _dtype(dy)
@@ -816,6 +831,7 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     need = (fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
             if (yp | 2 * ld) % 16 or (db | n_in) % 8 else 0)
     ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
-    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, wt,
-            out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
+    _launch(dev, "hx_weight_grad", fn.hx_weight_grad_bounded if bounded else fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens,
+            n_out, n_in, wt, out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need,
+            _status_ptr(status, dev), *bounded)
     return out

@@ -179,3 +179,12 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
                  lambda: hx.head_norm_rope_forward(x.view(1, 4, 8), 2, s, s, x, x, s)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_weight_grad_bounded_refuses_what_the_call_refuses():
+    w, bad = hx.lib().hx_weight_grad_bounded, hx.HX_ERR_ARG
+    tail = (10 ** 6, 0, None)
+    assert w(2, 2, A, 64, A, A, 128, 64, 32, 2, A, 32, 0, A, 1 << 30, None, *tail) == bad
+    assert w(0, 2, A, 65, A, A, 128, 64, 32, 2, A, 32, 0, None, 0, None, *tail) == bad
+    assert w(0, 2, A, 64, A, A, 128, 64, 32, 2, A, 31, 0, A, 1 << 30, None, *tail) == bad
+    assert w(0, 2, None, 64, None, None, 0, 64, 32, 2, A, 32, 1, None, 0, None, *tail) == 0
