@@ -24,8 +24,8 @@
 // brought it there: CTA pairs (each CTA converts and reads half of the tile's columns), several steps in conversion
 // at once, no fence wider than the CTA's own shared memory, whole-line stores.
 //
-// Every wait is bounded (2 s); when one runs out the CTA raises HX_ERR_TIMEOUT, waits for its own
-// copies in flight, frees its TMEM and returns. Its cluster's part of the result is NaN then: whatever sums it has are
+// Every wait is bounded (2 s); when one runs out the CTA raises HX_ERR_TIMEOUT, waits for the copies and products
+// in flight, frees its TMEM and returns. Its cluster's part of the result is NaN then: whatever sums it has are
 // not whole.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -231,6 +231,7 @@ struct Tile {
 struct Barriers {
   uint64_t copied[8], converted[8], empty[8], done;
   uint32_t tmem, failed;
+  uint32_t issued[2];  // in a pair's first CTA: the steps whose copies each CTA asked for
 };
 
 // ---------------------------------------------------------------------------------- conversion
@@ -410,6 +411,27 @@ __device__ __forceinline__ void join_rows(const Args& a, uint32_t tiles, uint32_
   }
 }
 
+// After giving up: a phase that completes by itself, in kWaitNs from t0 at most.
+__device__ __forceinline__ void wait_out(uint32_t bar, uint32_t parity, uint64_t t0) {
+  while (!bar_try(bar, parity) && now_ns() - t0 < kWaitNs) {
+  }
+}
+// After giving up, in a pair's first CTA (whose barriers count both CTAs' copies): waits for all copies on their way. n0 and
+// n1: the steps that it and the second CTA asked for. A step that only one of them asked for gets what its barrier misses.
+template <uint32_t kStages, uint32_t kBytes>
+__device__ __noinline__ void settle_copies(uint32_t bars, uint32_t n0, uint32_t n1) {
+  const uint64_t t0 = now_ns();
+  const uint32_t low = min(n0, n1), high = max(n0, n1);
+  for (uint32_t i = high > kStages ? high - kStages : 0; i < high; ++i) {
+    const uint32_t bar = bars + i % kStages * 8;
+    if (i >= low && n0 < n1)  // announced by nobody
+      bar_expect(bar, kBytes);
+    else if (i >= low)  // announced for both
+      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(kBytes) : "memory");
+    wait_out(bar, (i / kStages) & 1, t0);
+  }
+}
+
 // NaN to rows y0 .. y1 - 1 of each of the CTA's MT accumulators (rows m0 + i * M ..).
 template <typename O, int MT, uint32_t M, uint32_t N>
 __device__ __noinline__ void lose_rows(const Args& a, uint32_t m0, uint32_t n0, uint32_t y0, uint32_t y1) {
@@ -455,6 +477,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     }
     bar_init(done, 1);
     bars.failed = 0;
+    bars.issued[0] = bars.issued[1] = steps;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarps + 1) {
@@ -609,12 +632,8 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       if (k == steps)
         for (uint32_t i = k; i < k + S::kStages; ++i)
           if (!bar_wait(empty(i % S::kStages), ((i / S::kStages) & 1) ^ 1, failed, a.wait_ns)) break;
-      if (k < steps && rank == 0) {  // gave up: wait for the copies already on their way (a pair's, for both)
-        const uint64_t t0 = now_ns();
-        for (uint32_t i = k > S::kStages ? k - S::kStages : 0; i < k; ++i)
-          while (!bar_try(copied(i % S::kStages), (i / S::kStages) & 1) && now_ns() - t0 < kWaitNs) {
-          }
-      }
+      if (k < steps)  // gave up
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(smem_addr(&bars.issued[rank]), first)), "r"(k) : "memory");
     }
   } else if (rank == 0) {
     // the whole warp walks the steps, so that what the products take stays in uniform registers; one lane issues
@@ -639,11 +658,6 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
     // the products issued so far end before the TMEM is freed, also when a wait ran out. (Without steps nobody waits for
     // `done`: an arrival in the pair's other CTA could then come after that CTA's end.)
     if (steps && elected()) commit<kPair>(done, first);
-    if (!ok && lane == 0) {
-      const uint64_t t0 = now_ns();
-      while (!bar_try(done, 0) && now_ns() - t0 < kWaitNs) {
-      }
-    }
   }
   // a CTA that gave up tells its whole cluster: before the cluster's barrier, so that all know it after
   __syncwarp();
@@ -654,11 +668,17 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
   const bool lost = *failed, joined = MT == 1 && a.splits > 1;
   const uint32_t y0 = joined ? split * 128 / a.splits : 0, y1 = joined ? (split + 1) * 128 / a.splits : 128;
   if (lost) {
+    // no CTA ends before its copies and the products issued have
+    if (warp == kWarps && lane == 0 && rank == 0)
+      settle_copies<S::kStages, S::kA>(smem_addr(&bars.copied[0]), bars.issued[0], bars.issued[kPair]);
+    if (warp == kWarps + 1 && lane == 0 && steps) wait_out(done, 0, now_ns());
     if (a.dw_dtype == HX_F32)
       lose_rows<float, MT, S::M, S::N>(a, m0, n0, y0, y1);
     else
       lose_rows<T, MT, S::M, S::N>(a, m0, n0, y0, y1);
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
+    __syncwarp();
+    cluster_sync();
   } else if (joined) {
     // this split's share of the rows: the splits' sums in their order, four columns per thread
     if (a.dw_dtype == HX_F32)
