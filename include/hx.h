@@ -427,8 +427,9 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
  * An X beyond f16's range counts as +-65504 with HX_F16. d_workspace:
  * hx_weight_grad_workspace() bytes (0: may be NULL), 16-byte aligned, clobbered; needed for rows of dY that do not
  * start on 16 bytes, or of X on 8, which are copied first.
- * Waits inside the kernel are bounded (2 s): when one runs out, that part of d_dw is NaN, and HX_ERR_TIMEOUT is raised in
- * *d_status (NULL: the NaN alone tell). tokens = 0: zeros (or the old values). n_out <= 2^23, n_in <= 2^22. */
+ * Waits inside the kernel are bounded (2 s, of which time that the GPU gives another context hardly counts): when one
+ * runs out, that part of d_dw is NaN, and HX_ERR_TIMEOUT is raised in *d_status (NULL: the NaN alone tell). tokens = 0:
+ * zeros (or the old values). n_out <= 2^23, n_in <= 2^22. */
 uint64_t hx_weight_grad_workspace(const void* d_dy, uint64_t ld_dy, const uint8_t* d_bytes, uint64_t tokens,
                                   uint64_t n_out, uint64_t n_in);
 int hx_weight_grad(uint32_t format, uint32_t dtype, const void* d_dy, uint64_t ld_dy,

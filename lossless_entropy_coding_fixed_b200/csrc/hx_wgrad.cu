@@ -109,14 +109,17 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for the phase of `parity` to complete. False once this wait, or any other of the CTA, ran out.
+// Waits for the phase of `parity` to complete. False once this wait, or any other of the CTA, ran out. The timer goes on
+// while the GPU runs another context, so what passes between two looks at it counts as 1/64 of the limit at most.
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* failed, uint64_t limit) {
-  const uint64_t t0 = now_ns();
+  uint64_t last = now_ns(), spent = 0;
   for (;;) {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 16; ++i)
       if (bar_try(bar, parity)) return true;
     if (*failed) return false;
-    if (now_ns() - t0 > limit) {
+    const uint64_t t = now_ns();
+    spent += min(t - last, limit / 64 + 1), last = t;
+    if (spent > limit) {
       *failed = 1;
       return false;
     }
