@@ -903,11 +903,16 @@ int hx_weight_grad_bounded(uint32_t format, uint32_t dtype, const void* d_dy, ui
     if (!fn) return HX_ERR_CUDA;
     const cuuint64_t dims[2] = {n_out, tokens}, strides[1] = {pitch};
     const cuuint32_t box[2] = {64, kStep}, unit[2] = {1, 1};
-    if (fn(&map, dtype == HX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-           const_cast<void*>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return HX_ERR_CUDA;
+    const auto encode = [&] {
+      return fn(&map, dtype == HX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                const_cast<void*>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult rc = encode();
+    // a host thread's first CUDA call: the runtime makes the device's context current, a driver call does not
+    int dev = 0;
+    if (rc == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) rc = encode();
+    if (rc != CUDA_SUCCESS) return HX_ERR_CUDA;
   }
   return dtype == HX_F16 ? run<__half>(p, map, a, s) : run<__nv_bfloat16>(p, map, a, s);
 }

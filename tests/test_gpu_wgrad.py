@@ -228,6 +228,26 @@ def test_launches_back_to_back(cuda):
     assert int(st.item()) == 0 and all(torch.equal(out, want) for *_, want, out in cases)
 
 
+def test_on_a_new_host_thread(cuda):
+    """A thread's first CUDA call: nothing has made the device's context current there."""
+    import threading
+
+    dy, b, s = setup(256, 256, 256, "bf16", "e4m3", cuda)
+    want, out, raised = hx.weight_grad(dy, b, s), torch.zeros(256, 256, dtype=torch.bfloat16, device=cuda), []
+
+    def call():
+        try:
+            hx.weight_grad(dy, b, s, out=out)
+        except Exception as e:
+            raised.append(e)
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not raised and torch.equal(out, want)
+
+
 def test_status_stays_clear(cuda):
     dy, b, s = setup(300, 200, 100, "bf16", "e4m3", cuda)
     st = hx.new_status(cuda)
