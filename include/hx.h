@@ -423,7 +423,10 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
  * ld_dw) = dY^T X, plus d_dw's old values if accumulate. d_dy: tokens x n_out (row stride ld_dy), dtype
  * HX_F16 or HX_BF16; X: d_bytes (tokens x n_in) and d_scale; dw_dtype: HX_F32 or dtype. The products run
  * on the tensor cores in dtype: X's values are exact there for e4m3 rows in bf16 (and in f16 within its
- * normal range), and for INT8 rows held as a sum of two (17 bits in bf16, 22 in f16); sums are in 32 bits.
+ * normal range; below it, within 2^-25), and for INT8 rows held as a sum of two (within 2^-17 of each value in bf16, 2^-23 of
+ * it and 2^-36 in f16). Sums are in 32 bits, but the tensor cores cut what lies below them as they add 16 tokens at a time:
+ * a result is within (tokens + 64) 2^-23 of the sum of its terms' magnitudes (measured: a tenth of that), beside its own
+ * rounding. An f16 X below 2^-14 counts as 2^-14 there.
  * An X beyond f16's range counts as +-65504 with HX_F16. d_workspace:
  * hx_weight_grad_workspace() bytes (0: may be NULL), 16-byte aligned, clobbered; needed for rows of dY that do not
  * start on 16 bytes, or of X on 8, which are copied first.

@@ -12,7 +12,10 @@
 // The bytes never exist as a 16-bit matrix in memory. s_t q in bf16 is exact for e4m3 (the scale is a
 // power of two). For INT8 it is not, and one rounding to bf16 would put an error of the size of the result's
 // own rounding into every product: there the tile is held as two, the rounded values and the rounded
-// rest (17 bits together in bf16, 22 in f16), at twice the products. Sums are the tensor core's 32-bit accumulators.
+// rest (17 bits together in bf16), at twice the products. In f16 the rest of a value below 2^-3 would be below f16's normal
+// range, so it is held 2^11 times as large, with accumulators of its own (together 2^-23 of the value, and 2^-36).
+// Sums are the tensor core's 32-bit accumulators. It cuts what lies below their 32 bits each time it adds 16 tokens, so that
+// a sum of terms of one sign falls short: 8e-7 of it after 8192 tokens, 1.2e-5 after 2^16, 5e-4 after 2^20 (measured).
 //
 // Few tiles: the tokens are split over up to 8 CTAs (4 pairs) of one cluster, which leave their 32-bit partial
 // tiles in shared memory, and each adds the others' share of its rows in their order: no workspace, no second kernel.
@@ -32,6 +35,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "hx.h"
 #include "hx_values.h"
@@ -158,7 +162,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
         : "memory");
 }
 // The products of one stage of 64 tokens; kFirst: the tile's first.
-template <typename S, typename T, int MT, bool kPair, int kParts, bool kFirst>
+template <typename S, typename T, int MT, bool kPair, int kParts, int kSums, bool kFirst>
 __device__ __forceinline__ void stage_products(uint32_t tmem, uint32_t a, uint32_t b) {
   constexpr uint32_t instr = instruction<T, S::M, S::N>();
 #pragma unroll
@@ -168,10 +172,11 @@ __device__ __forceinline__ void stage_products(uint32_t tmem, uint32_t a, uint32
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {
         const uint32_t x = a + ((mt * 16384 + kk * 2048) >> 4), y = b + ((p * S::kB + kk * 2048) >> 4);
-        if (kFirst && kk == 0 && p == 0)
-          mma<kPair, false>(tmem + mt * S::N, x, y, instr);
+        const uint32_t d = tmem + (p % kSums * MT + mt) * S::N;
+        if (kFirst && kk == 0 && p < kSums)
+          mma<kPair, false>(d, x, y, instr);
         else
-          mma<kPair, true>(tmem + mt * S::N, x, y, instr);
+          mma<kPair, true>(d, x, y, instr);
       }
 }
 __device__ __forceinline__ bool elected() {
@@ -209,7 +214,8 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
 // A CTA, or a pair of CTAs on two SMs of one cluster, per tile. MT accumulators of 128 rows per CTA; 128
 // columns of X in each CTA's shared memory. A pair's products take both CTAs' columns (the second CTA's
 // through the pair's own path): 256 columns, each converted and read from shared memory by one CTA only.
-template <int MT, bool kPair, int kParts>
+// kSums: accumulators per 128 rows, 2 where X's second part has its own.
+template <int MT, bool kPair, int kParts, int kSums>
 struct Tile {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int M = 128 * kCtas, N = 128 * kCtas;  // of one product
@@ -225,7 +231,7 @@ struct Tile {
   static constexpr int kWarps = kGroups * kGroupWarps;
   static constexpr int kTokens = kStep / kGroupWarps;  // a converting warp's tokens of its step
   static constexpr int kThreads = 32 * (kWarps + 2);
-  static constexpr int kCols = MT * N;  // TMEM columns: a power of two of at least 32
+  static constexpr int kCols = MT * N * kSums;  // TMEM columns: a power of two of at least 32
   static constexpr int kSmem = kStages * kStage + 1024;
   static_assert(kStages * kStage >= kWarps * 4096, "");  // the epilogue's rows
   static_assert(kStages >= 3 && kGroups <= kStages && kCols <= 512 && (kCols & (kCols - 1)) == 0, "");
@@ -237,13 +243,18 @@ struct Barriers {
   uint32_t issued[2];  // in a pair's first CTA: the steps whose copies each CTA asked for
 };
 
-// ---------------------------------------------------------------------------------- conversion
-// 8 bytes of a row with scale s as values of type T, in kParts parts (1: e4m3, 2: INT8).
+// Whether T's second part of a value is held kRestUp times as large, and summed by itself.
+constexpr float kRestUp = 2048.0f;
 template <typename T, int kParts>
+constexpr bool kRestApart = kParts == 2 && Type<T>::kInf == 0x7c00u;
+
+// ---------------------------------------------------------------------------------- conversion
+// 8 bytes of a row with scale s as values of type T, in kParts parts (1: e4m3, 2: INT8). kClamp: they may pass T's range.
+template <typename T, int kParts, bool kClamp>
 __device__ __forceinline__ void convert(const Bytes<8>& b, float s, uint4 (&out)[kParts]) {
   float f[8];
   to_values<8>(kParts == 1 ? HX_ROWS_E4M3 : HX_ROWS_INT8, b, s, f);
-  if constexpr (Type<T>::kInf == 0x7c00u) {
+  if constexpr (kClamp) {
     // a row near fp16's largest value can round above it in its byte
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = f[i] > 65504.0f ? 65504.0f : f[i] < -65504.0f ? -65504.0f : f[i];
@@ -257,6 +268,7 @@ __device__ __forceinline__ void convert(const Bytes<8>& b, float s, uint4 (&out)
       if (p + 1 < kParts) {  // what the rounding left
         const float2 v = unpack2<T>(r[i]);
         f[2 * i] -= v.x, f[2 * i + 1] -= v.y;
+        if (kRestApart<T, kParts>) f[2 * i] *= kRestUp, f[2 * i + 1] *= kRestUp;
       }
     }
     out[p] = make_uint4(r[0], r[1], r[2], r[3]);
@@ -297,10 +309,22 @@ __device__ __forceinline__ void put(uint32_t addr, const uint4& v) {
 }
 
 // ------------------------------------------------------------------------------------ the tile
+// 32 columns of a lane's sums; kRest: the columns from there to the sums of the second parts, or 0.
+template <uint32_t kRest>
+__device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&r)[32]) {
+  tmem_load32(addr, r);
+  if constexpr (kRest != 0) {
+    uint32_t q[32];
+    tmem_load32(addr + kRest, q);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(fmaf(__uint_as_float(q[i]), 1.0f / kRestUp, __uint_as_float(r[i])));
+  }
+}
+
 // A warp's 32 rows of C = 128 / sizeof(O) columns from TMEM (columns tm ..) to the matrix o (n_rows x n_cols, row
 // stride ld) at (row, col). The rows pass through 4 KB of shared memory, so that the stores are whole lines (a lane
 // per row straight from TMEM would touch 32 lines with each store).
-template <typename O>
+template <typename O, uint32_t kRest>
 __device__ __forceinline__ void store_block(uint32_t stage, uint32_t tm, bool any, O* o, uint64_t ld, bool wide, bool add,
                                             uint32_t row, uint32_t col, uint32_t n_rows, uint32_t n_cols) {
   constexpr uint32_t C = 128 / sizeof(O);
@@ -309,7 +333,7 @@ __device__ __forceinline__ void store_block(uint32_t stage, uint32_t tm, bool an
 #pragma unroll
     for (uint32_t h = 0; h < C / 32; ++h) {
       uint32_t r[32];
-      tmem_load32(tm + h * 32, r);
+      load_sums<kRest>(tm + h * 32, r);
       constexpr uint32_t kChunks = 32 * sizeof(O) / 16, kPer = 16 / sizeof(O);
 #pragma unroll
       for (uint32_t c = 0; c < kChunks; ++c) {
@@ -358,7 +382,7 @@ __device__ __forceinline__ void store_block(uint32_t stage, uint32_t tm, bool an
     // onto old values: 32-bit sums through shared memory, 32 columns at a time, so that the total rounds once
     for (uint32_t h = 0; h < C / 32; ++h) {
       uint32_t r[32];
-      tmem_load32(tm + h * 32, r);
+      load_sums<kRest>(tm + h * 32, r);
 #pragma unroll
       for (uint32_t c = 0; c < 8; ++c)
         put(stage + lane * 128 + ((c ^ (lane & 7)) << 4),
@@ -447,9 +471,11 @@ __device__ __noinline__ void lose_rows(const Args& a, uint32_t m0, uint32_t n0, 
 }
 
 template <typename T, int MT, bool kPair, int kParts>
-__global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
+__global__ void __launch_bounds__(Tile<MT, kPair, kParts, 1 + kRestApart<T, kParts>>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a) {
-  using S = Tile<MT, kPair, kParts>;
+  constexpr int kSums = 1 + kRestApart<T, kParts>;
+  using S = Tile<MT, kPair, kParts, kSums>;
+  constexpr uint32_t kRest = kSums > 1 ? MT * S::N : 0;
   constexpr int kGroups = S::kGroups, kGroupWarps = S::kGroupWarps, kWarps = S::kWarps, kTokens = S::kTokens;
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bars;
@@ -551,13 +577,19 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
         for (int j = 0; j < kLoads; ++j)
           put(B + j * 256 + (swap ^ ((2 * j & 7) << 4)), convert_packed<T>(b[j], __shfl_sync(0xffffffffu, s2, 2 * j + odd)));
       } else {
+        const auto put_all = [&](auto clamp) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-          uint4 v[kParts];
-          convert<T, kParts>(b[j], __shfl_sync(0xffffffffu, sc, 2 * j + odd), v);
+          for (int j = 0; j < kLoads; ++j) {
+            uint4 v[kParts];
+            convert<T, kParts, decltype(clamp)::value>(b[j], __shfl_sync(0xffffffffu, sc, 2 * j + odd), v);
 #pragma unroll
-          for (int p = 0; p < kParts; ++p) put(B + p * S::kB + j * 256 + (swap ^ ((2 * j & 7) << 4)), v[p]);
-        }
+            for (int p = 0; p < kParts; ++p) put(B + p * S::kB + j * 256 + (swap ^ ((2 * j & 7) << 4)), v[p]);
+          }
+        };
+        if (Type<T>::kInf == 0x7f80u || (kParts == 2 && __all_sync(0xffffffffu, sc <= 65504.0f / 128)))
+          put_all(std::false_type{});
+        else
+          put_all(std::true_type{});
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -579,7 +611,7 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
         // the partial tile: 128 rows of N sums, 16-byte chunks exchanged within eights by the row
         for (uint32_t i = warp >> 2; i < S::N / 32; i += kWarps / 4) {
           uint32_t r[32];
-          tmem_load32(tmem + (quarter << 16) + i * 32, r);
+          load_sums<kRest>(tmem + (quarter << 16) + i * 32, r);
           const uint32_t y = quarter + lane;
 #pragma unroll
           for (uint32_t c = 0; c < 8; ++c)
@@ -595,10 +627,10 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
           const uint32_t tm = tmem + (quarter << 16) + mt * S::N + c;
           if (row >= a.n_out || col >= a.n_in) continue;
           if (a.dw_dtype == HX_F32)
-            store_block<float>(stage, tm, steps > 0, static_cast<float*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col,
+            store_block<float, kRest>(stage, tm, steps > 0, static_cast<float*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col,
                                a.n_out, a.n_in);
           else
-            store_block<T>(stage, tm, steps > 0, static_cast<T*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col, a.n_out,
+            store_block<T, kRest>(stage, tm, steps > 0, static_cast<T*>(a.dw), a.ld_dw, a.dw_wide, a.accumulate, row, col, a.n_out,
                            a.n_in);
         }
       }
@@ -650,9 +682,9 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts>::kThreads, 1)
       const uint32_t at = s * (S::kStage >> 4);
       if (elected()) {
         if (k == 0)
-          stage_products<S, T, MT, kPair, kParts, true>(tmem, a0 + at, b0 + at);
+          stage_products<S, T, MT, kPair, kParts, kSums, true>(tmem, a0 + at, b0 + at);
         else
-          stage_products<S, T, MT, kPair, kParts, false>(tmem, a0 + at, b0 + at);
+          stage_products<S, T, MT, kPair, kParts, kSums, false>(tmem, a0 + at, b0 + at);
         commit<kPair>(empty(s), first);
       }
       __syncwarp();
@@ -764,7 +796,7 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 template <typename T, int MT, bool kPair, int kParts>
 int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  using S = Tile<MT, kPair, kParts>;
+  using S = Tile<MT, kPair, kParts, 1 + kRestApart<T, kParts>>;
   const auto kernel = k_wgrad<T, MT, kPair, kParts>;
   if (!allow_shared<k_wgrad<T, MT, kPair, kParts>>(S::kSmem)) return HX_ERR_CUDA;
   const uint64_t ctas = ceil_div(a.n_out, S::BM) * ceil_div(a.n_in, S::BN) * S::kCtas * a.splits;
@@ -786,7 +818,11 @@ int launch_tile(const CUtensorMap& map, const Args& a, cudaStream_t s) {
 }
 template <typename T, int MT, bool kPair>
 int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
-  return a.fmt == HX_ROWS_E4M3 ? launch_tile<T, MT, kPair, 1>(map, a, s) : launch_tile<T, MT, kPair, 2>(map, a, s);
+  if (a.fmt == HX_ROWS_E4M3) return launch_tile<T, MT, kPair, 1>(map, a, s);
+  if constexpr (MT == 2 && kRestApart<T, 2>)
+    return HX_ERR_ARG;  // plan() does not give it: its sums would need 1024 columns of TMEM
+  else
+    return launch_tile<T, MT, kPair, 2>(map, a, s);
 }
 
 // The tile and the number of splits of the tokens, by the estimated time: rounds of CTAs over the SMs, each
@@ -798,12 +834,14 @@ int launch(const CUtensorMap& map, const Args& a, cudaStream_t s) {
 //   4096 x 1024 x 1024  27.3 / 28.4 / 44.1;  256 x 256 in 3 splits 18.0, 128 x 128 in 2 18.8
 //   8192 x 2048 x 2048  95.8 / 51.2 / 79.9
 //   4096 x 4096 x 4096  183 / 114 / 94
+// INT8 rows in f16 have two accumulators per 128 rows, and the 512 x 256 tile no room for them: 4096^3 199 us (bf16, with
+// that tile, 182), 300 x 8192 x 8192 154 (104).
 struct Plan {
   int mt;
   bool pair;
   uint32_t splits;
 };
-Plan plan(uint32_t fmt, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+Plan plan(uint32_t fmt, bool rest_apart, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
   struct Kind {
     int mt;
     bool pair;
@@ -818,6 +856,7 @@ Plan plan(uint32_t fmt, uint64_t tokens, uint64_t n_out, uint64_t n_in) {
   Plan best{1, false, 1};
   uint64_t least = ~0ull;
   for (const Kind& k : kinds) {
+    if (k.mt == 2 && rest_apart) continue;  // twice the accumulators do not fit
     const uint64_t ctas = ceil_div(n_out, k.rows) * ceil_div(n_in, k.cols) * (k.pair ? 2 : 1);
     const uint64_t most = k.mt == 2 ? 1 : kMaxCluster / (k.pair ? 2 : 1);
     for (uint64_t s = 1; s <= most && s <= std::max<uint64_t>(1, steps); ++s) {
@@ -877,7 +916,7 @@ int hx_weight_grad_bounded(uint32_t format, uint32_t dtype, const void* d_dy, ui
   if (need.dy + need.x && (!d_workspace || !multiple(d_workspace, 16) || workspace_bytes < need.dy + need.x))
     return HX_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Plan p = plan(format, tokens, n_out, n_in);
+  const Plan p = plan(format, format == HX_ROWS_INT8 && dtype == HX_F16, tokens, n_out, n_in);
   Args a{};
   a.fmt = format, a.bytes = d_bytes, a.ld_x = n_in, a.scale = d_scale;
   a.tokens = tokens, a.n_out = (uint32_t)n_out, a.n_in = (uint32_t)n_in;

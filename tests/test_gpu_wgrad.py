@@ -228,6 +228,29 @@ def test_launches_back_to_back(cuda):
     assert int(st.item()) == 0 and all(torch.equal(out, want) for *_, want, out in cases)
 
 
+@pytest.mark.parametrize("size", [(1, 40, 72), (3, 130, 264), (70, 515, 261), (40, 1664, 1664)])
+@pytest.mark.parametrize("level", [300.0, 1.0, 2.0 ** -4, 1e-3, 1e-4, 1e-5, 1e-7])
+def test_int8_rows_in_f16_at_every_level(cuda, size, level):
+    """X is held as two f16 values, the second 2^11 times as large: each value within 2^-23 of itself and 2^-36, after
+    one rounding of scale times byte to 32 bits (2^-24). Joining the two sums rounds once more. Sums as above, but relative to
+    terms of at least 2^-14 |dY|: the tensor core aligns a term by its factors' exponents, and that of a subnormal f16 is
+    2^-14's. (Two tokens, X = 2^-24 in both, dY = 1 and 2^-6 (1 + 2^-10): the terms' sum has its last bit at 2^-40 = 2^-26 of
+    2^-14, and the result lacks it; with 2^-5 in place of 2^-6 the last bit is at 2^-39, and the result has it. Relative to
+    the larger term itself, 2^-24, 16 bits would have been kept.)"""
+    T, n, k = size
+    g = torch.Generator(device=cuda).manual_seed(T)
+    dy = torch.randn(T, n, generator=g, device=cuda).half()
+    b, s = hx.quantize_rows(level * (2 * torch.rand(T, k, generator=g, device=cuda) - 1), hx.ROWS_INT8)
+    x, d = b.view(torch.int8).double() * s.double()[:, None], dy.double()
+    want, mags = d.T @ x, d.abs().T @ x.abs().clamp(min=2.0 ** -14)
+    tol = mags * ((T + 4) * 2.0 ** -23) + (d.abs().sum(0) * 2.0 ** -36)[:, None]
+    dw = hx.weight_grad(dy, b, s, hx.ROWS_INT8, dtype=torch.float32)
+    assert ((dw.double() - want).abs() <= tol).all()
+    old = torch.randn(n, k, generator=g, device=cuda) * level
+    dw = hx.weight_grad(dy, b, s, hx.ROWS_INT8, out=old.clone(), accumulate=True)
+    assert ((dw.double() - want - old.double()).abs() <= tol + (want + old.double()).abs() * 2.0 ** -24).all()
+
+
 def test_on_a_new_host_thread(cuda):
     """A thread's first CUDA call: nothing has made the device's context current there."""
     import threading
