@@ -94,14 +94,21 @@ __global__ void __launch_bounds__(512)
 }
 
 // ----------------------------------------------------------------------------- gated forward
-// silu(g) = g / (1 + e^-g). The exponential and the quotient are the fast ones (2 ulp each), far below
-// the output's own rounding for 16-bit types and at 32 bits' own noise for 32.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// silu(g) = g p with p = sigmoid(g) = 1 / (1 + e^-g), and 1 - p = sigmoid(-g). Both from e^-|g|, so that the quotient is
+// one by 1 to 2: of e^-g itself, it would be by numbers that pass 2^126 from g = -87.3 on, where the fast one is 0.
+// The exponential and the quotient are the fast ones: 2 + 1.173 |g| and 2 units of the last place.
+struct Sigmoid {
+  float p, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+  const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e), t = e * r;
+  return g >= 0.0f ? Sigmoid{r, t} : Sigmoid{t, r};
+}
 
 template <int W>
 __device__ __forceinline__ void gate(const float (&g)[W], const float (&u)[W], float (&h)[W]) {
 #pragma unroll
-  for (int i = 0; i < W; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
+  for (int i = 0; i < W; ++i) h[i] = g[i] * sigmoid(g[i]).p * u[i];
 }
 
 // At most 64 registers for 16-bit types: the compiler's 100 for bf16 and INT8 made 33554 x 1000 values 53 us, not 45.
@@ -281,10 +288,11 @@ __global__ void __launch_bounds__(kFlatThreads)
     to_values<W>(fmt, bu[i], su, fu);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const float s = sigmoid(fg[j]), silu = fg[j] * s;
+      const Sigmoid s = sigmoid(fg[j]);
+      const float silu = fg[j] * s.p;
       fh[j] = silu * fu[j];
       // dg into fu, du into fd
-      fu[j] *= fd[j] * fmaf(silu, 1.0f - s, s);
+      fu[j] *= fd[j] * fmaf(silu, s.rest, s.p);
       fd[j] *= silu;
     }
     store<T, W>(o + (uint64_t)v * W, fu);

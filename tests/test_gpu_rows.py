@@ -233,6 +233,32 @@ def test_many_rows(cuda, shape, dt):
     assert (np.abs(got[:, 1] - du) <= np.abs(du) * (half_step(dt) + 2.0 ** -18) + 1e-37).all()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gates_whose_exponential_is_huge(cuda, dt):
+    """e^-g between 2^126 and 2^128 and beyond, with an up value that makes the result an ordinary number. e^-|g| is then
+    below 2^-126: its last place is 2^-149, 2^-20 of it down to g = -89."""
+    g = np.array([-86, -87, -87.5, -88, -88.5, -89.0, 86, 87.5, 88])
+    u = np.array([1e30, -1e30, 2.0 ** 120])
+    gg, uu = (v.reshape(-1) for v in np.meshgrid(g, u))
+    x = torch.from_numpy(np.stack([np.concatenate([gg, uu])] * 3)).to(DT[dt]).to(cuda)
+    xs = x.double().cpu().numpy().reshape(3, 2, -1)
+    near = half_step(dt) + 2.0 ** -23 * (1.173 * 89 + 8) + 2.0 ** -20
+    for save in (True, False):
+        h = hx.gated_forward(x, save=save)[0].double().cpu().numpy()
+        want = ref.gated(xs[:, 0], xs[:, 1])
+        assert (np.abs(h - want) <= near * np.abs(want)).all()
+    for fmt, name in ((hx.ROWS_E4M3, "e4m3"), (hx.ROWS_INT8, "int8")):
+        _, b, s = hx.gated_forward(x, fmt)
+        dx, h = hx.gated_backward(torch.full((3, gg.size), 0.5, dtype=DT[dt], device=cuda), b, s, fmt, need_h=True)
+        v = ref.values(b.cpu().numpy(), s.cpu().numpy(), name)
+        want = ref.gated(v[:, 0], v[:, 1])
+        assert (np.abs(h.double().cpu().numpy() - want) <= near * np.abs(want)).all()
+        dg, du = ref.gated_grad(v[:, 0], v[:, 1], 0.5)
+        dx = dx.double().cpu().numpy().reshape(3, 2, -1)
+        assert (np.abs(dx[:, 0] - dg) <= near * np.abs(dg)).all()
+        assert (np.abs(dx[:, 1] - du) <= near * np.abs(du) + SUB[dt]).all()
+
+
 def test_gated_output_given(cuda):
     """An output of the caller's on a start that is not aligned; nothing beside it is written."""
     x = make(11, 2 * 264, "bf16", 6, cuda)
