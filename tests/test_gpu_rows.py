@@ -259,6 +259,36 @@ def test_gates_whose_exponential_is_huge(cuda, dt):
         assert (np.abs(dx[:, 1] - du) <= near * np.abs(du) + SUB[dt]).all()
 
 
+def test_gated_in_32_bits(cuda):
+    """f32: e^-|g| is within 2 units of the last place (4 2^-24); 1 + e^-|g| inherits half of that at most (2 2^-24) and
+    rounds (1); the quotient is within 2 units (4); its product with e^-|g|, the one with g and the one with u round (3):
+    14 2^-24 at most."""
+    g = torch.Generator(device=cuda).manual_seed(5)
+    gate = 160 * torch.rand(64, 4096, generator=g, device=cuda) - 80
+    up = torch.randn(64, 4096, generator=g, device=cuda)
+    for save in (True, False):
+        h = hx.gated_forward(torch.cat((gate, up), 1), save=save)[0].double().cpu().numpy()
+        want = ref.gated(gate.double().cpu().numpy(), up.double().cpu().numpy())
+        assert (np.abs(h - want) <= 14 * 2.0 ** -24 * np.abs(want)).all()
+    b, s = hx.quantize_rows(torch.stack((gate, up), 1).view(128, 4096), hx.ROWS_INT8)
+    dh = torch.randn(64, 4096, generator=g, device=cuda)
+    b, s = b.view(64, 2, 4096), s.view(64, 2)
+    # the values that the kernel reads: byte times scale, rounded to 32 bits
+    v = hx.dequantize_rows(b.view(128, 4096), s.view(128), hx.ROWS_INT8, dtype=torch.float32).double().cpu().numpy()
+    v = v.reshape(64, 2, 4096)
+    d = dh.double().cpu().numpy()
+    dx, h = hx.gated_backward(dh, b, s, hx.ROWS_INT8, need_h=True)
+    want = ref.gated(v[:, 0], v[:, 1])
+    assert (np.abs(h.double().cpu().numpy() - want) <= 14 * 2.0 ** -24 * np.abs(want)).all()
+    dg, du = ref.gated_grad(v[:, 0], v[:, 1], d)
+    dx = dx.double().cpu().numpy().reshape(64, 2, 4096)
+    p = ref.sigmoid(v[:, 0])
+    terms = np.abs(d * v[:, 1]) * (p + np.abs(v[:, 0]) * p * ref.sigmoid(-v[:, 0]))
+    assert (np.abs(dx[:, 1] - du) <= 14 * 2.0 ** -24 * np.abs(du)).all()
+    # p is within 12, silu within 13, 1 - p within 12: their product (one operation with the sum: 1), then dh u (2)
+    assert (np.abs(dx[:, 0] - dg) <= 28 * 2.0 ** -24 * terms).all()
+
+
 def test_gated_output_given(cuda):
     """An output of the caller's on a start that is not aligned; nothing beside it is written."""
     x = make(11, 2 * 264, "bf16", 6, cuda)
