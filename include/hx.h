@@ -383,7 +383,8 @@ int hx_gated_backward(uint32_t format, uint32_t dtype, const void* d_dout, uint6
  *   row d_positions[t] of d_cos and d_sin: (a, b) -> (a cos - b sin, b cos + a sin). Pair i is
  *   (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.
  * dim: even, 2..512; rot_dim: even, 0..dim. The sum of x^2 is held in 32 bits: a head for which it passes them
- * (values from 2^64 / sqrt(dim) on) is saved as any other, but its y and dx are 0 or NaN. */
+ * (values from 2^64 / sqrt(dim) on) is saved as any other, but its y and dx are 0 or NaN. With an eps below 2^-126, r
+ * loses bits where mean(x^2) falls below that too (values from 2^-63 down). */
 typedef struct {
   uint32_t format;         /* HX_ROWS_*                                                       */
   uint32_t dtype;          /* of x and y (dy and dx)                                          */

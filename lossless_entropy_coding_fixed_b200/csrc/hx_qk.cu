@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_backward(const __grid_consta
       }
       float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
       group_sums(sq, dot, a.lanes);
-      sq *= scale * scale, dot *= scale;
+      sq = sq * scale * scale, dot *= scale;  // (the scale's square alone falls out of 32 bits long before the sum does)
       float r = rsqrtf(fmaf(sq, part, a.eps));
       if (!ok) r = __uint_as_float(0x7fc00000u);
       const float sr = scale * r;                // n = q sr

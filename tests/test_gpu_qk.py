@@ -43,6 +43,10 @@ def setup(T, nq, nk, D, R, dt, cuda, seed=0, wdt=torch.float32, places=None, pdt
                 pos=to(rng.integers(0, places, T), pdt))
 
 
+def half(dt):
+    return torch.finfo(DT[dt]).eps / 2
+
+
 def args(p, nq):
     return (nq, p["wq"], p["wk"], p["cos"], p["sin"], p["pos"])
 
@@ -115,6 +119,35 @@ def test_forward_and_backward(cuda, case, dt, inter):
     assert n1 is None and n2 is None and torch.equal(y, y2)
     got = hx.head_norm_rope_backward(p["dy"], b, s, *args(p, nq), eps=EPS, interleaved=inter, fmt=FMT[fmt])
     check_backward(*got, b, s, p, nq, dt, inter, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("level", [-30, -60, -64, -66, -68])
+def test_backward_of_tiny_heads_without_eps(cuda, level, dt, fmt):
+    """Rows whose scale squared is below 32 bits' numbers, but not their mean square. That is at least 2^-137 here; its
+    last place is 2^-149, so that it is within 2^-13 where it is below 2^-126, and its inverse root within 2^-14: three of
+    those in dx, one in a weight gradient."""
+    p = setup(6, 2, 1, 64, 32, dt, cuda, seed=9)
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(rng.choice([-1, 1], (18, 64)) * rng.uniform(0.8, 1.2, (18, 64)) * 2.0 ** level).to(DT[dt]).to(cuda)
+    b, s = hx.quantize_rows(x, FMT[fmt])
+    b, s = b.view(6, 3, 64), s.view(6, 3)
+    dx, dwq, dwk = hx.head_norm_rope_backward(p["dy"], b, s, *args(p, 2), eps=0.0, fmt=FMT[fmt])
+    v, dy, (c, sn) = ref.values(b.cpu().numpy(), f64(s), fmt), f64(p["dy"]), angles(p)
+    wq, wk = f64(p["wq"]), f64(p["wk"])
+    want, wdq, wdk = ref.head_norm_rope_grad(dy, v, 2, wq, wk, c, sn, 0.0, False)
+    r = 1 / np.sqrt(np.mean(v * v, -1, keepdims=True))
+    i, j = ref.pair_places(32, False)
+    g = np.abs(dy).copy()
+    g[..., i] = g[..., j] = np.abs(dy[..., i]) + np.abs(dy[..., j])
+    d = g * np.abs(ref.head_weights(3, 2, wq, wk))
+    xn = np.abs(v * r)
+    lost = 2.0 ** -14 if level < -62 else 0
+    assert (np.abs(f64(dx) - want) <= np.abs(want) * half(dt) + r * (d + xn * np.mean(d * xn, -1, keepdims=True)) *
+            (2.0 ** -19 + 3 * lost)).all()
+    for got, w, lo, hi in ((dwq, wdq, 0, 2), (dwk, wdk, 2, 3)):
+        assert (np.abs(f64(got) - w) <= (g * xn)[:, lo:hi].sum((0, 1)) * (2.0 ** -18 + lost)).all()
 
 
 @pytest.mark.parametrize("wdt", [torch.float32, torch.bfloat16])
