@@ -28,7 +28,8 @@ class _Entry:
 
 
 class CheckpointStore:
-    """Coded 8-bit rows by key. All calls of a store are made on one CUDA stream. `hist` (int32[256] on the
+    """Coded 8-bit rows by key, on the device of the table block, whichever is current. All calls of a store are made on one
+    CUDA stream. `hist` (int32[256] on the
     device), if given, accumulates the histogram of all bytes put, for the next codebook. Errors in the data
     (a byte without a code, a stream that does not decode) are kept on the device until seal() or check() reads
     them; what take() gave before that is not to be relied on."""
@@ -46,6 +47,8 @@ class CheckpointStore:
         import torch
         if data.dtype is not torch.uint8 or not data.is_contiguous():
             raise TypeError("data must be contiguous uint8")
+        if data.device != self.tables.device:
+            raise ValueError("data must be on the table block's device")
         flat = data.view(-1)
         n = flat.numel()
         if n >= 1 << 32:
@@ -53,7 +56,8 @@ class CheckpointStore:
         need = hx.scratch_bytes(n)
         if self._scratch is None or self._scratch.numel() < need:
             self._scratch = torch.empty(need, dtype=torch.uint8, device=data.device)
-        stream, status = hx.encode(self.tables, flat, scratch=self._scratch, hist=self.hist, kind=self.kind)
+        with torch.cuda.device(self.tables.device):  # the coder launches on the current device
+            stream, status = hx.encode(self.tables, flat, scratch=self._scratch, hist=self.hist, kind=self.kind)
         key, self._next = self._next, self._next + 1
         self._entries[key] = _Entry(stream, scale, status, tuple(data.shape))
         return key
@@ -91,7 +95,8 @@ class CheckpointStore:
         for d in e.shape:
             n *= d
         out = torch.empty(max(n, 1), dtype=torch.uint8, device=e.stream.device)[:n]
-        hx.decode(self.tables, e.stream, n, out=out, status=self._status, kind=self.kind)
+        with torch.cuda.device(self.tables.device):
+            hx.decode(self.tables, e.stream, n, out=out, status=self._status, kind=self.kind)
         return out.view(e.shape), e.scale
 
     def check(self) -> None:
