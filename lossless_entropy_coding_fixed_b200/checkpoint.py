@@ -43,7 +43,9 @@ class CheckpointStore:
 
     def put(self, data, scale) -> int:
         """Codes the bytes of 8-bit rows and keeps them with their scales; returns their key. `data` is not
-        needed afterwards. Fewer than 2^32 bytes, contiguous, aligned as a torch allocation."""
+        needed afterwards. `scale` is kept as it is, not copied: take() gives back the same tensor, so it must not be
+        written until then (quantize_rows(x, scale=buffer) with one buffer for several layers needs a clone here).
+        check() does not notice. Fewer than 2^32 bytes, contiguous, aligned as a torch allocation."""
         import torch
         if data.dtype is not torch.uint8 or not data.is_contiguous():
             raise TypeError("data must be contiguous uint8")
