@@ -94,19 +94,21 @@ __global__ void __launch_bounds__(512)
 }
 
 // ----------------------------------------------------------------------------- gated forward
-// silu(g) = g p with p = sigmoid(g) = 1 / (1 + e^-g), and 1 - p = sigmoid(-g). Both from e^-|g|, so that the quotient is
-// one by 1 to 2: of e^-g itself, it would be by numbers that pass 2^126 from g = -87.3 on, where the fast one is 0.
-// The quotient is the fast one (2 units of the last place), and for 16-bit types so is the exponential: 2 + 1.173 |g| units,
-// 2^-16 of the result at most. For f32 it is expf (2 units): as fast in wide units, odd widths take up to a tenth longer
-// (33554 x 1001 saved as e4m3 115 us, 109 with the fast one).
+// silu(g) = g p with p = sigmoid(g) = e / (1 + e) and 1 - p = 1 / (1 + e), e = e^g. g is held below 80, where p is 1, so that
+// 1 + e stays far from 2^126, from where on the fast quotient is 0 (1 / (1 + e^-g) is there from g = -87.3 on).
+// The quotient is the fast one (1 unit of the last place), and for 16-bit types so is the exponential: 2 + 1.173 |g| units,
+// 2^-16 of the result at most. For f32 it is expf (2 units).
 struct Sigmoid {
-  float p, rest;
+  float g, p, rest;  // g held below 80; a NaN stays in all three
 };
 template <typename T>
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
-  const float e = sizeof(T) == 4 ? expf(-fabsf(g)) : __expf(-fabsf(g));
-  const float r = __fdividef(1.0f, 1.0f + e), t = e * r;
-  return g >= 0.0f ? Sigmoid{r, t} : Sigmoid{t, r};
+  Sigmoid s;
+  asm("min.NaN.f32 %0, %1, 0f42A00000;" : "=f"(s.g) : "f"(g));
+  const float e = sizeof(T) == 4 ? expf(s.g) : __expf(s.g);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.rest) : "f"(1.0f + e));
+  s.p = e * s.rest;
+  return s;
 }
 
 template <typename T, int W>
@@ -116,7 +118,7 @@ __device__ __forceinline__ void gate(const float (&g)[W], const float (&u)[W], f
 }
 
 // At most 64 registers, for two blocks per SM: the compiler's 100 for bf16 and INT8 made 33554 x 1000 values 53 us, not 45,
-// its 70 for f32 and INT8 8192 x 8192 values 209 us, not 156.
+// its 70 for f32 and INT8 8192 x 8192 values 209 us, not 151.
 template <typename T, int W, int R, bool kBlock, bool kLong, uint32_t fmt>
 __global__ void __launch_bounds__(512, 2)
     k_gated_save(const T* __restrict__ x, uint64_t rows, uint32_t cols, uint64_t ld,
@@ -261,9 +263,11 @@ __global__ void __launch_bounds__(kFlatThreads)
   }
 }
 
-// h = g p u with p = sigmoid(g): dg = dh u p (1 + g (1 - p)), du = dh g p.
+// h = g p u with p = sigmoid(g): dg = dh u p (1 + g (1 - p)), du = dh g p. 64 registers in units of 8, for four blocks per SM
+// (the compiler's 80 made 33554 x 1000 values 44.4 us, not 42.6). Smaller units have none stated (0): with one block per SM
+// stated the compiler takes 96, and 33554 x 1001 values 120 us, not 75.
 template <typename T, int W, int U>
-__global__ void __launch_bounds__(kFlatThreads)
+__global__ void __launch_bounds__(kFlatThreads, W == 8 ? 4 : 0)
     k_gated_backward(uint32_t fmt, const T* __restrict__ dh, uint64_t ld, const uint8_t* __restrict__ bytes,
                      const float* __restrict__ scale, const Tasks t, T* __restrict__ dx, T* __restrict__ h) {
   const Task k = task_of<W, U>(t);
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kFlatThreads)
       const float silu = fg[j] * s.p;
       fh[j] = silu * fu[j];
       // dg into fu, du into fd
-      fu[j] *= fd[j] * fmaf(silu, s.rest, s.p);
+      fu[j] *= fd[j] * fmaf(s.g * s.p, s.rest, s.p);
       fd[j] *= silu;
     }
     store<T, W>(o + (uint64_t)v * W, fu);
