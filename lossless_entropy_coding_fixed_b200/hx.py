@@ -793,19 +793,6 @@ def weight_grad(dy, data, scale, fmt: int = ROWS_E4M3, out=None, dtype=None, acc
     8-bit rows of its input X [tokens, n_in]. The result has `dtype` (dy's, or float32), or goes to the
     matrix `out`, onto its old values if `accumulate`. If a wait inside the kernel runs out (2 s; it does not, on a sound
     GPU), that part of the result is NaN, and HX_ERR_TIMEOUT is raised in `status`, if given."""
-    return _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status)
-
-
-def weight_grad_bounded(dy, data, scale, wait_ns: int, withhold: int = (1 << 64) - 1, fmt: int = ROWS_E4M3, out=None,
-                        dtype=None, accumulate: bool = False, status=None):
-    """hx_weight_grad_bounded: weight_grad() with its waits' limit in nanoseconds and, for failure tests, a block of the
-    launch (`withhold`) whose part never counts as ready. Returns (result, status)."""
-    if status is None:
-        status = new_status(dy.device)
-    return _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status, (wait_ns, withhold)), status
-
-
-def _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status, bounded=()):
     torch = _torch or _load_torch()
     dev = _device(dy, "dy")
     dt = _dtype(dy)
@@ -831,7 +818,28 @@ def _weight_grad(dy, data, scale, fmt, out, dtype, accumulate, status, bounded=(
     need = (fn.hx_weight_grad_workspace(yp, ld, db, tokens, n_out, n_in)
             if (yp | 2 * ld) % 16 or (db | n_in) % 8 else 0)
     ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
-    _launch(dev, "hx_weight_grad", fn.hx_weight_grad_bounded if bounded else fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens,
-            n_out, n_in, wt, out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need,
-            _status_ptr(status, dev), *bounded)
+    _launch(dev, "hx_weight_grad", fn.hx_weight_grad, fmt, dt, yp, ld, db, sp, tokens, n_out, n_in, wt,
+            out.data_ptr(), ldw, 1 if accumulate else 0, ws.data_ptr() if need else None, need, _status_ptr(status, dev))
     return out
+
+
+def weight_grad_bounded(dy, data, scale, out, wait_ns: int, withhold: int = (1 << 64) - 1, fmt: int = ROWS_E4M3,
+                        accumulate: bool = False, status=None):
+    """hx_weight_grad_bounded: weight_grad() into `out` with its waits' limit in nanoseconds and, for failure tests, a
+    block of the launch (`withhold`) whose part never counts as ready. Returns (out, status)."""
+    torch = _torch or _load_torch()
+    dev = _device(dy, "dy")
+    tokens, n_out, ld = _matrix(dy, "dy")
+    _device(data, "bytes")
+    n_in = data.shape[-1]
+    db = _dense(data, "bytes", (tokens, n_in), torch.uint8, dev)
+    sp = _dense(scale, "scale", (tokens,), torch.float32, dev)
+    _same(out, "out", (n_out, n_in), out.dtype, dev)
+    if status is None:
+        status = new_status(dy.device)
+    need = lib().hx_weight_grad_workspace(dy.data_ptr(), ld, db, tokens, n_out, n_in)
+    ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    _launch(dev, "hx_weight_grad_bounded", lib().hx_weight_grad_bounded, fmt, _dtype(dy), dy.data_ptr(), ld, db, sp, tokens,
+            n_out, n_in, _dtype(out), out.data_ptr(), _matrix(out, "out")[2], 1 if accumulate else 0, ws.data_ptr(), need,
+            _status_ptr(status, dev), wait_ns, withhold)
+    return out, status

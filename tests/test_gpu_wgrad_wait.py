@@ -42,7 +42,7 @@ def test_withheld_block_leaves_nan(cuda, case, accumulate, which):
     for dt in (torch.bfloat16, torch.float32):
         old = torch.randn(n, k, device=cuda).to(dt)
         want = hx.weight_grad(dy, b, s, FMT[fmt], out=old.clone(), accumulate=accumulate)
-        got, st = hx.weight_grad_bounded(dy, b, s, WAIT, block, FMT[fmt], out=old.clone(), accumulate=accumulate)
+        got, st = hx.weight_grad_bounded(dy, b, s, old.clone(), WAIT, block, FMT[fmt], accumulate=accumulate)
         assert int(st.item()) == hx.HX_ERR_TIMEOUT
         lost = torch.isnan(got)
         assert torch.equal(torch.where(lost, want, got), want)
@@ -61,8 +61,9 @@ def test_withheld_block_leaves_nan(cuda, case, accumulate, which):
 def test_no_withheld_block(cuda):
     for case in CASES:
         dy, b, s = setup(*case[:4], cuda)
-        got, st = hx.weight_grad_bounded(dy, b, s, 10 ** 9, 1 << 40, FMT[case[3]])
-        assert int(st.item()) == 0 and torch.equal(got, hx.weight_grad(dy, b, s, FMT[case[3]]))
+        want = hx.weight_grad(dy, b, s, FMT[case[3]])
+        got, st = hx.weight_grad_bounded(dy, b, s, torch.empty_like(want), 10 ** 9, 1 << 40, FMT[case[3]])
+        assert int(st.item()) == 0 and torch.equal(got, want)
 
 
 def test_without_a_status_word_the_result_tells(cuda):
