@@ -16,8 +16,10 @@
 //
 // Measured on B200, 8192 tokens of 32 + 8 heads of 128 in bf16, e4m3 rows: forward 39.6 us, backward 49.3 with the weight
 // gradients; the bytes at the measured copy rate take 32.7. Without the copies ahead 45.8 and 57.4, whatever
-// arithmetic was left out: too few loads in flight. What is left is the backward pass's registers (two blocks of 256 threads per SM;
-// three spill).
+// arithmetic was left out: too few loads in flight. Of the forward pass's loads a third are for nothing: past an item's last
+// head the copies ahead go to that head again (L2 answers them). Backward, registers hold it to two blocks of 256 threads per SM
+// (120; three blocks spill and take 102 us). At these limits single values per vector spill up to 116 bytes backward, and INT8 from
+// bf16 or f32 up to 24 forward.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -715,10 +717,9 @@ int check(const Args& a, uint32_t dtype, uint32_t w_dtype, uint32_t pos_bits) {
 
 // The lanes per head: a power of two with 16 values each. Heads per item: 8, so that a token's
 // angles and the weight are loaded once for them, halved while the items would not fill the GPU.
-void arrange(Args* a, int pu, int sms) {
+void arrange(Args* a, int sms) {
   uint32_t lanes = 1;
   while (lanes * 16 < a->dim) lanes *= 2;
-  (void)pu;
   a->lanes = lanes;
   a->per = 8;
   const uint64_t want = (uint64_t)sms * (1024 / lanes);
@@ -755,7 +756,7 @@ int hx_head_norm_rope_forward(const hx_head_norm_rope* p, const void* d_x, uint6
   const int sms = sm_count();
   if (!sms) return HX_ERR_CUDA;
   const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2, p->interleaved != 0);
-  arrange(&a, pu, sms);
+  arrange(&a, sms);
   const uint64_t items = a.tokens * (ceil_div(a.nq, a.per) + ceil_div(a.nk, a.per));
   return run(false, p->dtype, pu, p->interleaved != 0, a, ceil_div(items, kThreads / a.lanes),
              static_cast<cudaStream_t>(stream));
@@ -791,7 +792,7 @@ int hx_head_norm_rope_backward(const hx_head_norm_rope* p, const void* d_dy, uin
   uint64_t blocks = 0;
   if (a.tokens) {
     const int pu = vector_of(a, p->dtype == HX_F32 ? 4 : 2, p->interleaved != 0);
-    arrange(&a, pu, sms);
+    arrange(&a, sms);
     // two blocks per SM hold all groups that fit at once; queries and keys share them by heads
     const uint64_t groups = kThreads / a.lanes;
     const uint64_t bq = ceil_div(a.tokens * ceil_div(a.nq, a.per), groups);

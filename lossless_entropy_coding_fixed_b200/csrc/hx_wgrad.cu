@@ -22,8 +22,9 @@
 //
 // Rows of dY that do not start on 16 bytes (TMA's rule), or of X on 8, are first copied to rows that do.
 //
-// Measured on B200 (bf16): 8192 x 8192 x 8192 from e4m3 rows 666-680 us = 1.62-1.65 PFLOP/s, cuBLAS on two bf16 matrices 660-675 on
-// the same machine; both run at its power limit (990 W). 4096^3 93 us; INT8, at twice the products, 172 and 1267 us. What
+// Measured on B200 (bf16): 8192 x 8192 x 8192 from e4m3 rows 655-680 us in short runs, 790 us over seconds at the power
+// limit (1425 MHz, 993 W); cuBLAS on two bf16 matrices 660-675 and 793 (1327 MHz) on the same machine. 4096^3 94 us. INT8, at
+// twice the products: 4096^3 182 us; 8192^3 1260-1290 us in short runs, 1504 over seconds (1417 MHz, 995 W). What
 // brought it there: CTA pairs (each CTA converts and reads half of the tile's columns), several steps in conversion
 // at once, no fence wider than the CTA's own shared memory, whole-line stores.
 //
