@@ -54,7 +54,7 @@ typedef enum {
   HX_ERR_UNCODABLE = 4,  /* encode: an input byte has no code word (seen-only codebook)      */
   HX_ERR_CORRUPT = 8,    /* decode: the stream is malformed or does not decode exactly      */
   HX_ERR_CODEBOOK = 16,  /* decode: the stream was written with another codebook or kind    */
-  HX_ERR_TIMEOUT = 32,   /* encode: a bounded wait for the chunks before one ran out          */
+  HX_ERR_TIMEOUT = 32,   /* a bounded wait on the device ran out (encode, weight gradient)     */
   HX_ERR_CAPACITY = 64   /* encode: out_cap is too small; header.total_words holds the need */
 } hx_status;
 
