@@ -94,33 +94,32 @@ __global__ void __launch_bounds__(512)
 }
 
 // ----------------------------------------------------------------------------- gated forward
-// silu(g) = g p with p = sigmoid(g) = e / (1 + e) and 1 - p = 1 / (1 + e), e = e^g. g is held below 80, where p is 1, so that
-// 1 + e stays far from 2^126, from where on the fast quotient is 0 (1 / (1 + e^-g) is there from g = -87.3 on).
+// silu(g) = g p with p = sigmoid(g) = 1 / (1 + e^-g), and 1 - p = sigmoid(-g). Both from e = e^-|g|: 1 / (1 + e) and
+// e / (1 + e), so that the quotient is one by 1 to 2 (of e^-g itself it would be by numbers that pass 2^126 from g = -87.3 on,
+// where the fast one is 0), and p is exactly 1 for large g, where a product g u of 16-bit values can lie at a half.
 // The quotient is the fast one (1 unit of the last place). For f32 e is expf (2 units). For 16-bit types it is the fast 2^x, for bf16
 // its square at half the exponent: 4 units and 0.75 |g| more (the exponent's rounding), 2^-16 of the result at most. The fast
 // 2^x is 0 below 2^-126, which half the exponent reaches at g = -174; the one that is not costs two operations more (bf16
-// 8192 x 8192, sustained: 84.5 us, not 82.3). With f16, whose values end at 65504, nothing is left of p below 2^-126.
+// 8192 x 8192, sustained: 84.5 us, not 82.9). With f16, whose values end at 65504, nothing is left of p below 2^-126.
 struct Sigmoid {
-  float g, p, rest;  // g held below 80; a NaN stays in all three
+  float p, rest;
 };
 template <typename T>
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
-  Sigmoid s;
-  asm("min.NaN.f32 %0, %1, 0f42A00000;" : "=f"(s.g) : "f"(g));
-  float e, sum;
+  float e, sum, r;
   if constexpr (sizeof(T) == 4) {
-    e = expf(s.g), sum = 1.0f + e;
+    e = expf(-fabsf(g)), sum = 1.0f + e;
   } else if constexpr (!Type<T>::kWide) {
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s.g * 1.44269504f));  // 1 / ln 2
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(g) * -1.44269504f));  // 1 / ln 2
     sum = 1.0f + e;
   } else {
     float half;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(half) : "f"(s.g * 0.72134752f));  // 1 / (2 ln 2)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(half) : "f"(fabsf(g) * -0.72134752f));  // 1 / (2 ln 2)
     e = half * half, sum = fmaf(half, half, 1.0f);
   }
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.rest) : "f"(sum));
-  s.p = e * s.rest;
-  return s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sum));
+  const float t = e * r;
+  return g >= 0.0f ? Sigmoid{r, t} : Sigmoid{t, r};
 }
 
 template <typename T, int W>
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kFlatThreads, W == 8 ? 4 : 0)
       const float silu = fg[j] * s.p;
       fh[j] = silu * fu[j];
       // dg into fu, du into fd
-      fu[j] *= fd[j] * fmaf(s.g * s.p, s.rest, s.p);
+      fu[j] *= fd[j] * fmaf(silu, s.rest, s.p);
       fd[j] *= silu;
     }
     store<T, W>(o + (uint64_t)v * W, fu);
