@@ -63,7 +63,7 @@ struct Args {
   uint32_t dw_dtype, accumulate, dw_wide;
   uint32_t splits, steps;
   uint32_t* status;
-  uint64_t wait_ns, withhold;  // a wait's limit; a CTA whose converting warps never arrive (tests)
+  uint64_t wait_ns, withhold;  // a wait's limit; a CTA whose converting warps do nothing (tests)
 };
 
 // ------------------------------------------------------------------------------------ barriers
@@ -440,36 +440,54 @@ __device__ __forceinline__ void join_rows(const Args& a, uint32_t tiles, uint32_
   }
 }
 
-// After giving up: a phase that completes by itself, in kWaitNs from t0 at most.
+// What follows a wait that ran out stands apart from the kernel's code, whose end then has nothing to skip (in line it cost
+// a launch 0.2 us or more).
+// To every CTA of the cluster: this one gave up.
+__device__ __noinline__ void tell_cluster(uint32_t failed, uint32_t ctas) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (lane < ctas) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(failed, lane)), "r"(1) : "memory");
+}
+// A phase that completes by itself, in kWaitNs from t0 at most.
 __device__ __forceinline__ void wait_out(uint32_t bar, uint32_t parity, uint64_t t0) {
   while (!bar_try(bar, parity) && now_ns() - t0 < kWaitNs) {
   }
 }
-// After giving up, in a pair's first CTA (whose barriers count both CTAs' copies): waits for all copies on their way. n0 and
-// n1: the steps that it and the second CTA asked for. A step that only one of them asked for gets what its barrier misses.
-template <uint32_t kStages, uint32_t kBytes>
-__device__ __noinline__ void settle_copies(uint32_t bars, uint32_t n0, uint32_t n1) {
-  const uint64_t t0 = now_ns();
-  const uint32_t low = min(n0, n1), high = max(n0, n1);
-  for (uint32_t i = high > kStages ? high - kStages : 0; i < high; ++i) {
-    const uint32_t bar = bars + i % kStages * 8;
-    if (i >= low && n0 < n1)  // announced by nobody
-      bar_expect(bar, kBytes);
-    else if (i >= low)  // announced for both
-      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(kBytes) : "memory");
-    wait_out(bar, (i / kStages) & 1, t0);
-  }
-}
-
-// NaN to rows y0 .. y1 - 1 of each of the CTA's MT accumulators (rows m0 + i * M ..).
-template <typename O, int MT, uint32_t M, uint32_t N>
-__device__ __noinline__ void lose_rows(const Args& a, uint32_t m0, uint32_t n0, uint32_t y0, uint32_t y1) {
+// NaN to rows y0 .. y1 - 1 of each of the CTA's accumulators (rows m0 + i * M ..).
+template <typename O>
+__device__ __forceinline__ void lose_rows(const Args& a, uint32_t m0, uint32_t n0, uint32_t y0, uint32_t y1, uint32_t mt,
+                                          uint32_t M, uint32_t N) {
   const O nan = Type<O>::from_f(__uint_as_float(0x7fc00000u));
-  for (uint32_t i = threadIdx.x; i < MT * (y1 - y0) * N; i += blockDim.x) {
-    const uint32_t y = i / N, mt = y / (y1 - y0);
-    const uint32_t row = m0 + mt * M + y0 + y % (y1 - y0), col = n0 + i % N;
+  for (uint32_t i = threadIdx.x; i < mt * (y1 - y0) * N; i += blockDim.x) {
+    const uint32_t y = i / N, row = m0 + y / (y1 - y0) * M + y0 + y % (y1 - y0), col = n0 + i % N;
     if (row < a.n_out && col < a.n_in) static_cast<O*>(a.dw)[(uint64_t)row * a.ld_dw + col] = nan;
   }
+}
+// All threads of all CTAs of a cluster in which a wait ran out: no CTA ends before its copies and the products issued have,
+// and its part of the result is NaN. In a pair's first CTA, whose barriers count both CTAs' copies, a step that only one of
+// them asked for gets what its barrier misses.
+template <typename S, typename T, int MT, bool kPair>
+__device__ __noinline__ void give_up(const Args& a, Barriers& bars, uint32_t steps, uint32_t rank, uint32_t m0, uint32_t n0,
+                                     uint32_t y0, uint32_t y1) {
+  const uint64_t t0 = now_ns();
+  if (threadIdx.x == 0 && rank == 0) {
+    const uint32_t one = bars.issued[0], two = bars.issued[kPair], low = min(one, two), high = max(one, two);
+    for (uint32_t i = high > S::kStages ? high - S::kStages : 0; i < high; ++i) {
+      const uint32_t bar = smem_addr(&bars.copied[i % S::kStages]);
+      if (i >= low && one < two)  // announced by nobody
+        bar_expect(bar, S::kA);
+      else if (i >= low)  // announced for both
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"((uint32_t)S::kA) : "memory");
+      wait_out(bar, (i / S::kStages) & 1, t0);
+    }
+  }
+  if (threadIdx.x == 32 && steps) wait_out(smem_addr(&bars.done), 0, t0);
+  if (a.dw_dtype == HX_F32)
+    lose_rows<float>(a, m0, n0, y0, y1, MT, S::M, S::N);
+  else
+    lose_rows<T>(a, m0, n0, y0, y1, MT, S::M, S::N);
+  if (threadIdx.x == 0 && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
+  __syncwarp();
+  cluster_sync();
 }
 
 template <typename T, int MT, bool kPair, int kParts>
@@ -555,10 +573,10 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts, 1 + kRestApart<T, kPar
         for (int j = 0; j < kLoads; ++j) b[j].load(x + min(t + 2 * j + odd, a.tokens - 1) * a.ld_x);
       }
     };
-    if (group < steps) fetch(group);
-    const bool tells = lane == 0 && blockIdx.x != a.withhold;
+    const uint32_t mine = blockIdx.x == a.withhold ? 0 : steps;
+    if (group < mine) fetch(group);
     bool ok = true;
-    for (uint32_t k = group; k < steps; k += kGroups) {
+    for (uint32_t k = group; k < mine; k += kGroups) {
       const uint32_t s = k % S::kStages;
       // one answer per warp: what follows is for whole warps
       if (!(ok = __all_sync(0xffffffffu, bar_wait(empty(s), ((k / S::kStages) & 1) ^ 1, failed, a.wait_ns)))) break;
@@ -595,13 +613,13 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts, 1 + kRestApart<T, kPar
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (tells) {
+      if (lane == 0) {
         if constexpr (kPair)
           bar_arrive_at(converted(s), first);
         else
           bar_arrive(converted(s));
       }
-      if (k + kGroups < steps) fetch(k + kGroups);
+      if (k + kGroups < mine) fetch(k + kGroups);
     }
     // ---- the tile's rows: lanes 32 (warp % 4) .. + 31 of TMEM
     if (ok && steps) ok = bar_wait(done, 0, failed, a.wait_ns);
@@ -665,10 +683,6 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts, 1 + kRestApart<T, kPar
                 : "memory");
         }
       }
-      // The last stages' releases: the first CTA of a pair sends them to the second too, where nothing else waits for them.
-      if (k == steps)
-        for (uint32_t i = k; i < k + S::kStages; ++i)
-          if (!bar_wait(empty(i % S::kStages), ((i / S::kStages) & 1) ^ 1, failed, a.wait_ns)) break;
       if (k < steps)  // gave up
         asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(smem_addr(&bars.issued[rank]), first)), "r"(k) : "memory");
     }
@@ -687,35 +701,24 @@ __global__ void __launch_bounds__(Tile<MT, kPair, kParts, 1 + kRestApart<T, kPar
           stage_products<S, T, MT, kPair, kParts, kSums, true>(tmem, a0 + at, b0 + at);
         else
           stage_products<S, T, MT, kPair, kParts, kSums, false>(tmem, a0 + at, b0 + at);
-        commit<kPair>(empty(s), first);
+        // only where somebody waits for it: an arrival in the pair's other CTA could else come after that CTA's end
+        if (k + S::kStages < steps) commit<kPair>(empty(s), first);
       }
       __syncwarp();
       if (++s == S::kStages) s = 0, parity ^= 1;
     }
-    // the products issued so far end before the TMEM is freed, also when a wait ran out. (Without steps nobody waits for
-    // `done`: an arrival in the pair's other CTA could then come after that CTA's end.)
+    // the products issued so far end before the TMEM is freed, also when a wait ran out. (Without steps nobody waits.)
     if (steps && elected()) commit<kPair>(done, first);
   }
   // a CTA that gave up tells its whole cluster: before the cluster's barrier, so that all know it after
   __syncwarp();
-  if (*failed && lane < S::kCtas * a.splits)
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(smem_addr(&bars.failed), lane)), "r"(1) : "memory");
+  if (__builtin_expect(*failed, 0)) tell_cluster(smem_addr(&bars.failed), S::kCtas * a.splits);
   __syncwarp();
   cluster_sync();
-  const bool lost = *failed, joined = MT == 1 && a.splits > 1;
+  const bool joined = MT == 1 && a.splits > 1;
   const uint32_t y0 = joined ? split * 128 / a.splits : 0, y1 = joined ? (split + 1) * 128 / a.splits : 128;
-  if (lost) {
-    // no CTA ends before its copies and the products issued have
-    if (warp == kWarps && lane == 0 && rank == 0)
-      settle_copies<S::kStages, S::kA>(smem_addr(&bars.copied[0]), bars.issued[0], bars.issued[kPair]);
-    if (warp == kWarps + 1 && lane == 0 && steps) wait_out(done, 0, now_ns());
-    if (a.dw_dtype == HX_F32)
-      lose_rows<float, MT, S::M, S::N>(a, m0, n0, y0, y1);
-    else
-      lose_rows<T, MT, S::M, S::N>(a, m0, n0, y0, y1);
-    if (threadIdx.x == 0 && a.status) atomicOr(a.status, (uint32_t)HX_ERR_TIMEOUT);
-    __syncwarp();
-    cluster_sync();
+  if (__builtin_expect(*failed, 0)) {
+    give_up<S, T, MT, kPair>(a, bars, steps, rank, m0, n0, y0, y1);
   } else if (joined) {
     // this split's share of the rows: the splits' sums in their order, four columns per thread
     if (a.dw_dtype == HX_F32)
